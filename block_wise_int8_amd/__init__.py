@@ -16,6 +16,11 @@ Entry points (same names as the C ABI, without the ``blockint8_`` prefix):
   :func:`moe_combine` -- the MoE steps around the grouped GEMM,
   :func:`moe_gemm_silu_quant` -- the w13 GEMM with the gating as its epilogue,
   and :func:`moe_layer`, the whole FusedMoE layer built from them
+* :func:`rmsnorm_quant` -- residual addition, RMS norm and quantisation (int8
+  or e4m3 codes), what feeds the linears and the MoE layer
+* :func:`quant_act_fp8`, :func:`gemm_fp8`, :func:`linear_fp8`,
+  :func:`moe_gemm_fp8`, :func:`moe_layer_fp8`, ... -- the e4m3 form of the same
+  layer (module :mod:`.fp8`)
 
 ``gemm`` and ``moe_gemm`` pick a kernel by shape (:func:`gemm_select`,
 :func:`moe_gemm_select`); their ``variant`` argument names one instead.
@@ -104,6 +109,8 @@ def load() -> ctypes.CDLL:
               "blockint8_moe_gemm_select", "blockint8_gemm_variant", "blockint8_moe_gemm_variant",
               "blockint8_moe_gemm_ws"):
         getattr(lib, f).restype = i32
+    fp8.declare(lib)
+    norm.declare(lib)
     _lib = lib
     return lib
 
@@ -570,3 +577,10 @@ def check_tp_partition(input_size: int, input_size_per_partition: int, output_pa
     sizes = (ctypes.c_int64 * len(output_partition_sizes))(*[int(v) for v in output_partition_sizes])
     _check(load().blockint8_check_tp_partition(int(input_size), int(input_size_per_partition), sizes,
                                                len(output_partition_sizes), int(tp_size), block[0], block[1]))
+
+
+from . import fp8, norm  # noqa: E402  (they use the names above)
+from .fp8 import *  # noqa: E402,F401,F403
+from .norm import *  # noqa: E402,F401,F403
+
+__all__ += fp8.__all__ + norm.__all__

@@ -1,0 +1,194 @@
+"""The e4m3 form of the block-scaled linear and MoE layer (``include/blockint8_fp8.h``).
+
+The functions of the int8 layer with ``torch.float8_e4m3fn`` codes in the place
+of int8 ones: the same shapes, scales, blocks ([128, 128]) and errors.
+"""
+from __future__ import annotations
+
+import torch
+
+import block_wise_int8_amd as _bi8
+
+from . import _call as c
+
+__all__ = ["quant_act_fp8", "quant_act_gather_fp8", "silu_mul_quant_fp8", "quant_weight_fp8", "gemm_fp8",
+           "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_fp8_workspace_size", "moe_layer_fp8"]
+
+FP8 = torch.float8_e4m3fn
+
+
+def declare(lib) -> None:
+    vp, i64, i32 = c.VP, c.I64, c.I32
+    c.declare(lib, "blockint8_quant_act_fp8", [vp, i64, i64, i64, i32, vp, vp, vp])
+    c.declare(lib, "blockint8_quant_act_gather_fp8", [vp, i64, i64, vp, i64, i64, i32, vp, vp, vp])
+    c.declare(lib, "blockint8_silu_mul_quant_fp8", [vp, i64, i64, i32, vp, vp, vp, vp])
+    c.declare(lib, "blockint8_quant_weight_fp8", [vp, i64, i64, i64, i32, i32, vp, vp, vp])
+    c.declare(lib, "blockint8_gemm_fp8", [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp])
+    c.declare(lib, "blockint8_gemm_fp8_workspace_size", [i64, i64, i64], i64)
+    c.declare(lib, "blockint8_linear_fp8", [vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, i64, vp])
+    c.declare(lib, "blockint8_moe_gemm_fp8", [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, vp])
+    c.declare(lib, "blockint8_moe_gemm_fp8_workspace_size", [i64, i64, i64, i32], i64)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // _bi8.BLOCK)
+
+
+def quant_act_fp8(x: torch.Tensor, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None):
+    """Dynamic quantisation of bf16 ``x`` [M, K], one scale per token and 128 columns.
+
+    Returns ``(xq float8_e4m3fn [M, K], xs float32 [M, ceil(K/128)])``.  ``x``
+    may have a row stride larger than K.
+    """
+    dev = c.device_of(x, "x")
+    M, K, ldx = c.rows(x, "x", dev)
+    xq = c.output(xq, "xq", dev, FP8, (M, K))
+    xs = c.output(xs, "xs", dev, torch.float32, (M, _blocks(K)))
+    _bi8._check(c.call(_bi8.load().blockint8_quant_act_fp8, dev, x.data_ptr(), M, K, ldx, 128, xq.data_ptr(),
+                       xs.data_ptr()))
+    return xq, xs
+
+
+def quant_act_gather_fp8(x: torch.Tensor, rows: torch.Tensor, xq: torch.Tensor | None = None,
+                         xs: torch.Tensor | None = None):
+    """quant_act_fp8 of the rows ``x[rows]`` (bf16 [T, K], int32 indices [R])."""
+    dev = c.device_of(x, "x")
+    T, K, ldx = c.rows(x, "x", dev)
+    c.dense(rows, "rows", dev, torch.int32, (None,))
+    R = rows.shape[0]
+    xq = c.output(xq, "xq", dev, FP8, (R, K))
+    xs = c.output(xs, "xs", dev, torch.float32, (R, _blocks(K)))
+    _bi8._check(c.call(_bi8.load().blockint8_quant_act_gather_fp8, dev, x.data_ptr(), T, ldx, rows.data_ptr(), R, K,
+                       128, xq.data_ptr(), xs.data_ptr()))
+    return xq, xs
+
+
+def silu_mul_quant_fp8(h: torch.Tensor, aq: torch.Tensor | None = None, as_: torch.Tensor | None = None,
+                       return_a: bool = False):
+    """h = [gate | up] bf16 [R, 2I] -> (aq float8_e4m3fn [R, I], as float32 [R, ceil(I/128)][, a bf16 [R, I]])."""
+    dev = c.device_of(h, "h")
+    c.dense(h, "h", dev, torch.bfloat16, (None, None))
+    R, two_i = h.shape
+    if two_i % 2:
+        raise ValueError("h must have an even number of columns (gate | up)")
+    I = two_i // 2
+    aq = c.output(aq, "aq", dev, FP8, (R, I))
+    as_ = c.output(as_, "as_", dev, torch.float32, (R, _blocks(I)))
+    a = torch.empty((R, I), dtype=torch.bfloat16, device=dev) if return_a else None
+    _bi8._check(c.call(_bi8.load().blockint8_silu_mul_quant_fp8, dev, h.data_ptr(), R, I, 128, aq.data_ptr(),
+                       as_.data_ptr(), c.ptr(a)))
+    return (aq, as_, a) if return_a else (aq, as_)
+
+
+def quant_weight_fp8(w: torch.Tensor):
+    """Block quantisation of a bf16 weight [N, K] -> (float8_e4m3fn [N, K], float32 [ceil(N/128), ceil(K/128)])."""
+    dev = c.device_of(w, "w")
+    N, K, ldw = c.rows(w, "w", dev)
+    wq = torch.empty((N, K), dtype=FP8, device=dev)
+    ws = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
+    _bi8._check(c.call(_bi8.load().blockint8_quant_weight_fp8, dev, w.data_ptr(), N, K, ldw, 128, 128, wq.data_ptr(),
+                       ws.data_ptr()))
+    return wq, ws
+
+
+def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace ``gemm_fp8`` uses for an M x N x K problem (0: none)."""
+    return int(_bi8.load().blockint8_gemm_fp8_workspace_size(M, N, K))
+
+
+def gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
+             bias: torch.Tensor | None = None, y: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Block-scaled e4m3 GEMM ``y = x . W^T (+ bias)`` -> bf16 [M, N].
+
+    ``workspace`` (any contiguous tensor on the device, of at least
+    ``gemm_fp8_workspace_size`` bytes) lets problems with few tiles split K
+    between workgroups; calls that share one must not overlap in time."""
+    dev = c.device_of(xq, "xq")
+    c.dense(xq, "xq", dev, FP8, (None, None))
+    M, K = xq.shape
+    c.dense(w, "w", dev, FP8, (None, K))
+    N = w.shape[0]
+    c.dense(xs, "xs", dev, torch.float32, (M, _blocks(K)))
+    c.dense(ws, "ws", dev, torch.float32, (_blocks(N), _blocks(K)))
+    if bias is not None:
+        c.dense(bias, "bias", dev, torch.bfloat16, (N,))
+    y = c.output(y, "y", dev, torch.bfloat16, (M, N))
+    wsp, nbytes = c.scratch(workspace, dev)
+    _bi8._check(c.call(_bi8.load().blockint8_gemm_fp8, dev, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(),
+                       c.ptr(bias), y.data_ptr(), M, N, K, 128, 128, wsp, nbytes))
+    return y
+
+
+def linear_fp8(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, bias: torch.Tensor | None = None,
+               y: torch.Tensor | None = None, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The e4m3 linear with dynamic activation scales -> bf16 [M, N]: quant_act_fp8
+    of bf16 ``x`` [M, K] into ``xq`` / ``xs`` (fresh tensors when not given;
+    they hold the quantised activations on return), then gemm_fp8, through one
+    C call.  ``workspace`` as for gemm_fp8."""
+    dev = c.device_of(x, "x")
+    M, K, ldx = c.rows(x, "x", dev)
+    c.dense(w, "w", dev, FP8, (None, K))
+    N = w.shape[0]
+    KB = _blocks(K)
+    c.dense(ws, "ws", dev, torch.float32, (_blocks(N), KB))
+    if bias is not None:
+        c.dense(bias, "bias", dev, torch.bfloat16, (N,))
+    y = c.output(y, "y", dev, torch.bfloat16, (M, N))
+    xq = c.output(xq, "xq", dev, FP8, (M, K))
+    xs = c.output(xs, "xs", dev, torch.float32, (M, KB))
+    wsp, nbytes = c.scratch(workspace, dev)
+    _bi8._check(c.call(_bi8.load().blockint8_linear_fp8, dev, x.data_ptr(), ldx, w.data_ptr(), ws.data_ptr(),
+                       c.ptr(bias), y.data_ptr(), M, N, K, 128, 128, xq.data_ptr(), xs.data_ptr(), wsp, nbytes))
+    return y
+
+
+def moe_gemm_fp8_workspace_size(R: int, N: int, K: int, E: int) -> int:
+    """Bytes of workspace ``moe_gemm_fp8`` can use for the grouped problem (0: none)."""
+    return int(_bi8.load().blockint8_moe_gemm_fp8_workspace_size(R, N, K, E))
+
+
+def moe_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Tensor,
+                 ws: torch.Tensor, y: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Grouped block-scaled e4m3 GEMM over expert-sorted rows -> bf16 [R, N].
+
+    ``expert_offsets`` is int32 [E+1] on the device (rows [off[e], off[e+1])
+    use expert e); ``w`` is float8_e4m3fn [E, N, K], ``ws`` float32 [E,
+    ceil(N/128), ceil(K/128)].  ``workspace`` as for gemm_fp8, of
+    ``moe_gemm_fp8_workspace_size`` bytes."""
+    dev = c.device_of(xq, "xq")
+    c.dense(xq, "xq", dev, FP8, (None, None))
+    R, K = xq.shape
+    c.dense(w, "w", dev, FP8, (None, None, K))
+    E, N, _ = w.shape
+    c.dense(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
+    c.dense(xs, "xs", dev, torch.float32, (R, _blocks(K)))
+    c.dense(ws, "ws", dev, torch.float32, (E, _blocks(N), _blocks(K)))
+    y = c.output(y, "y", dev, torch.bfloat16, (R, N))
+    wsp, nbytes = c.scratch(workspace, dev)
+    _bi8._check(c.call(_bi8.load().blockint8_moe_gemm_fp8, dev, xq.data_ptr(), xs.data_ptr(),
+                       expert_offsets.data_ptr(), w.data_ptr(), ws.data_ptr(), y.data_ptr(), R, N, K, E, 128, 128, wsp,
+                       nbytes))
+    return y
+
+
+def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor, w2: torch.Tensor,
+                  ws2: torch.Tensor, k: int, renormalize: bool = False) -> torch.Tensor:
+    """The e4m3 FusedMoE layer on the GPU: route, gather + quantise, w13 grouped
+    GEMM, SiLU gating + quantise, w2 grouped GEMM, weighted combine.  x bf16
+    [T, H]; logits fp32 [T, E]; w13 float8_e4m3fn [E, 2I, H]; w2 float8_e4m3fn
+    [E, H, I].  Returns bf16 [T, H]."""
+    dev = c.device_of(x, "x")
+    with torch.cuda.device(dev):
+        _, weights, sorted_token, offsets, row_of = _bi8.moe_route(logits, k, renormalize)
+        xq, xs = quant_act_gather_fp8(x, sorted_token)
+        R, H = xq.shape
+        E, N = w13.shape[:2]
+        nbytes = max(moe_gemm_fp8_workspace_size(R, N, H, E),
+                     moe_gemm_fp8_workspace_size(R, w2.shape[1], w2.shape[2], E))
+        wsp = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        aq, as_ = silu_mul_quant_fp8(moe_gemm_fp8(xq, xs, offsets, w13, ws13, workspace=wsp))
+        y2 = moe_gemm_fp8(aq, as_, offsets, w2, ws2, workspace=wsp)
+        return _bi8.moe_combine(y2, row_of, weights)
