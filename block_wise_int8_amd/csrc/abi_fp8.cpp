@@ -86,6 +86,15 @@ int32_t check_gemm_sizes(const char *fn, int64_t rows, int64_t N, int64_t K, int
     return check_block(fn, block_n, block_k);
 }
 
+int32_t check_variant(const char *fn, int32_t variant, int64_t K) {
+    if (variant < BI8_GEMM_AUTO || variant > BI8_GEMM_TILE_128X128)
+        return fail_status(BI8_ERR_SHAPE, "%s: unknown kernel variant %d", fn, variant);
+    if (K % 16 != 0 && variant != BI8_GEMM_AUTO)
+        return fail_status(BI8_ERR_ALIGN, "%s: K = %lld is not a multiple of 16; that form has one kernel (variant "
+                           "must be AUTO)", fn, (long long)K);
+    return BI8_OK;
+}
+
 int32_t rmsnorm_quant(const char *fn, bool fp8, const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,
                       const uint16_t *weight, double eps, int64_t M, int64_t H, int32_t block_k, uint16_t *h,
                       int64_t ldh, uint16_t *y, void *xq, float *xs, void *stream) {
@@ -179,18 +188,36 @@ int32_t blockint8_quant_weight_fp8(const uint16_t *w, int64_t N, int64_t K, int6
     return bi8::call_status(fn, bi8::launch_quant_weight_fp8(w, N, K, ldw, wq, ws, static_cast<hipStream_t>(stream)));
 }
 
-int32_t blockint8_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws, const uint16_t *bias,
-                           uint16_t *y, int64_t M, int64_t N, int64_t K, int32_t block_n, int32_t block_k,
-                           void *workspace, int64_t workspace_bytes, void *stream) {
+int32_t blockint8_gemm_fp8_select(int64_t M, int64_t N, int64_t K) {
+    return static_cast<int32_t>(bi8::select_gemm_fp8_path(M, N, K));
+}
+
+int32_t blockint8_moe_gemm_fp8_select(int64_t R, int64_t N, int64_t K, int32_t E) {
+    return static_cast<int32_t>(bi8::select_moe_gemm_fp8_path(R, N, K, E > 0 ? E : 1));
+}
+
+int32_t blockint8_gemm_fp8_variant(int32_t variant, const uint8_t *xq, const float *xs, const uint8_t *w,
+                                   const float *ws, const uint16_t *bias, uint16_t *y, int64_t M, int64_t N, int64_t K,
+                                   int32_t block_n, int32_t block_k, void *workspace, int64_t workspace_bytes,
+                                   void *stream) {
     static const char fn[] = "blockint8_gemm_fp8";
+    BI8_TRY(check_variant(fn, variant, K));
     BI8_TRY(check_gemm_sizes(fn, M, N, K, block_n, block_k));
     BI8_TRY(check_workspace(fn, workspace, workspace_bytes));
     if (M == 0) return done(fn);
     BI8_TRY(check_codes(fn, xq, xs));
     BI8_TRY(check_product(fn, w, ws, bias, y));
-    return bi8::call_status(fn, bi8::launch_gemm_fp8(xq, xs, w, ws, bias, y, M, N, K, static_cast<float *>(workspace),
+    return bi8::call_status(fn, bi8::launch_gemm_fp8(static_cast<bi8::Fp8Path>(variant), xq, xs, w, ws, bias, y, M, N,
+                                                     K, static_cast<float *>(workspace),
                                                      workspace ? workspace_bytes : 0,
                                                      static_cast<hipStream_t>(stream)));
+}
+
+int32_t blockint8_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws, const uint16_t *bias,
+                           uint16_t *y, int64_t M, int64_t N, int64_t K, int32_t block_n, int32_t block_k,
+                           void *workspace, int64_t workspace_bytes, void *stream) {
+    return blockint8_gemm_fp8_variant(BI8_GEMM_AUTO, xq, xs, w, ws, bias, y, M, N, K, block_n, block_k, workspace,
+                                      workspace_bytes, stream);
 }
 
 int64_t blockint8_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
@@ -214,16 +241,17 @@ int32_t blockint8_linear_fp8(const uint16_t *x, int64_t ldx, const uint8_t *w, c
     const hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e = bi8::launch_quant_act_fp8(x, M, ldx, nullptr, M, K, xq_workspace, xs_workspace, st);
     if (e == hipSuccess)
-        e = bi8::launch_gemm_fp8(xq_workspace, xs_workspace, w, ws, bias, y, M, N, K, static_cast<float *>(workspace),
+        e = bi8::launch_gemm_fp8(bi8::Fp8Path::kAuto, xq_workspace, xs_workspace, w, ws, bias, y, M, N, K, static_cast<float *>(workspace),
                                  workspace ? workspace_bytes : 0, st);
     return bi8::call_status(fn, e);
 }
 
-int32_t blockint8_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t *expert_offsets, const uint8_t *w,
-                               const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K, int32_t E,
-                               int32_t block_n, int32_t block_k, void *workspace, int64_t workspace_bytes,
-                               void *stream) {
+int32_t blockint8_moe_gemm_fp8_variant(int32_t variant, const uint8_t *xq, const float *xs,
+                                       const int32_t *expert_offsets, const uint8_t *w, const float *ws, uint16_t *y,
+                                       int64_t R, int64_t N, int64_t K, int32_t E, int32_t block_n, int32_t block_k,
+                                       void *workspace, int64_t workspace_bytes, void *stream) {
     static const char fn[] = "blockint8_moe_gemm_fp8";
+    BI8_TRY(check_variant(fn, variant, 16));
     if (E <= 0 || E > 65536) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 65536]", fn, E);
     BI8_TRY(check_gemm_sizes(fn, R, N, K, block_n, block_k));
     if (K % 16 != 0) return fail_status(BI8_ERR_ALIGN, "%s: K = %lld must be a multiple of 16", fn, (long long)K);
@@ -233,10 +261,18 @@ int32_t blockint8_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t
     BI8_TRY(check_align(fn, "expert_offsets", expert_offsets, 4));
     BI8_TRY(check_codes(fn, xq, xs));
     BI8_TRY(check_product(fn, w, ws, nullptr, y));
-    return bi8::call_status(fn, bi8::launch_moe_gemm_fp8(xq, xs, expert_offsets, w, ws, y, R, N, K, E,
-                                                         static_cast<float *>(workspace),
+    return bi8::call_status(fn, bi8::launch_moe_gemm_fp8(static_cast<bi8::Fp8Path>(variant), xq, xs, expert_offsets, w,
+                                                         ws, y, R, N, K, E, static_cast<float *>(workspace),
                                                          workspace ? workspace_bytes : 0,
                                                          static_cast<hipStream_t>(stream)));
+}
+
+int32_t blockint8_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t *expert_offsets, const uint8_t *w,
+                               const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K, int32_t E,
+                               int32_t block_n, int32_t block_k, void *workspace, int64_t workspace_bytes,
+                               void *stream) {
+    return blockint8_moe_gemm_fp8_variant(BI8_GEMM_AUTO, xq, xs, expert_offsets, w, ws, y, R, N, K, E, block_n, block_k,
+                                          workspace, workspace_bytes, stream);
 }
 
 int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, int32_t E) {

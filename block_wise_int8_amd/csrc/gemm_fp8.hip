@@ -223,6 +223,371 @@ hipError_t launch_skinny(const GemmArgs &p, int64_t rows, hipStream_t stream) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Tiled path
+// ---------------------------------------------------------------------------
+//
+// A workgroup of WN x WM waves computes a BN x BM tile (weight rows x
+// activation rows), each wave SA x SB sub-tiles of 32 x 32.  K advances one
+// block a step through a ring of NS stages in LDS, filled by buffer-to-LDS
+// loads NS - 1 blocks ahead: rows of 128 bytes, their 16-byte pieces
+// XOR-swizzled so that the fragment reads do not conflict.  Rows past the tile
+// and pieces past K read as zero through the buffer range check, on both
+// sides (a NaN code times zero would be NaN).
+//
+// The block sum of sub-tile j starts from zero, and is rescaled into the
+// running sum while the matrix core works on sub-tile j + 1; the last
+// sub-tile's rescale runs under the next block's barrier and first reads.
+// The activation scales reach LDS eight blocks at a time; the weight scale of
+// a wave's 128-row block is a scalar load one block ahead.
+template <int WN_, int WM_, int SA_, int SB_, int NS_>
+struct Cfg {
+    static constexpr int WN = WN_, WM = WM_, SA = SA_, SB = SB_, NS = NS_;
+    static constexpr int kWaves = WN * WM;
+    static constexpr int kThreads = kWaves * 64;
+    static constexpr int kWaveN = 32 * SA;
+    static constexpr int kWaveM = 32 * SB;
+    static constexpr int kBN = kWaveN * WN;
+    static constexpr int kBM = kWaveM * WM;
+    static constexpr int kXOff = kBN * 128;
+    static constexpr int kStageBytes = kXOff + kBM * 128;
+    static constexpr int kWLoads = kBN / 8 / kWaves;   // 1 KB pieces a wave loads
+    static constexpr int kXLoads = kBM / 8 / kWaves;
+    static constexpr int kLoads = kWLoads + kXLoads;
+    static constexpr int kSB = 8;                      // K blocks in a batch of scales
+    static constexpr int kScaleLoads = kBM * kSB / 64 / kWaves;
+    static_assert(kBN % (8 * kWaves) == 0 && kBM % (8 * kWaves) == 0, "load split");
+    static_assert(128 % kWaveN == 0, "a wave's weight rows lie in one scale block");
+    static_assert(kScaleLoads >= 1 && kBM * kSB % (64 * kWaves) == 0, "scale split");
+    static_assert(kWaves % 2 == 0, "a lane's pieces share their parity");
+    static_assert(NS >= 2 && NS <= 4 && NS - 2 < kSB, "ring depth");
+};
+
+// SPLIT: a workgroup sums only a run of K blocks and stores fp32 partial sums:
+// dense, run blockIdx.y of kb_per_split blocks, in p.partial[blockIdx.y];
+// grouped, the tiles of a partial last round (see tail_plan).
+template <class C, bool MOE, bool SPLIT, int64_t GM>
+__global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int SA = C::SA, SB = C::SB, NS = C::NS;
+    __shared__ __attribute__((aligned(1024))) char lds0[C::kStageBytes];
+    __shared__ __attribute__((aligned(1024))) char lds1[C::kStageBytes];
+    __shared__ __attribute__((aligned(1024))) char lds2[NS > 2 ? C::kStageBytes : 1];
+    __shared__ __attribute__((aligned(1024))) char lds3[NS > 3 ? C::kStageBytes : 1];
+    auto lds = [&](const int i) __attribute__((always_inline)) -> char * {
+        return i == 0 ? lds0 : i == 1 ? lds1 : i == 2 ? lds2 : lds3;
+    };
+    __shared__ float xsl[2][C::kBM * C::kSB];
+
+    Tile t;
+    if (!decode_tile<C::kBN, C::kBM, MOE, GM, MOE && SPLIT>(p, t)) return;
+    if (t.rows <= 0) return;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t K = p.K;
+    int64_t kb0 = 0, KB = p.KB;   // this workgroup's K blocks: [kb0, kb0 + KB)
+    if constexpr (SPLIT && !MOE) {
+        kb0 = (int64_t)blockIdx.y * p.kb_per_split;
+        KB = p.KB - kb0 < p.kb_per_split ? p.KB - kb0 : p.kb_per_split;
+    }
+    if constexpr (SPLIT && MOE) {
+        if (t.split >= 0) {
+            const int64_t per = (p.KB + t.nsplit - 1) / t.nsplit;
+            kb0 = (int64_t)t.split * per;
+            KB = p.KB - kb0 < per ? p.KB - kb0 : per;
+        }
+    }
+
+    // (ranges of at most 2^31 bytes: 256 rows of K <= 2^23)
+    const int64_t wrows = p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN;
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(t.w + t.n0 * K, clamp_bytes(wrows * K));
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
+
+    // Piece q (1 KB) covers tile rows [8q, 8q + 8): lane i lands at row 8q + i/8,
+    // 16-byte slot i % 8, which holds K piece slot ^ swz(row), swz(r) = (r & 7) ^
+    // ((r >> 3) & 1).  A wave's pieces q = wave + j kWaves share their parity,
+    // so a lane's K piece is the same in all of them.
+    const int r_in = lane >> 3;
+    const int chunk = 16 * ((lane & 7) ^ r_in ^ (wave & 1));
+    const uint32_t go = (uint32_t)((8 * wave + r_in) * K + kb0 * kBlock + chunk);
+    const uint32_t piece_stride = (uint32_t)(8 * C::kWaves * K);
+    uint32_t sofs[C::kScaleLoads];
+#pragma unroll
+    for (int j = 0; j < C::kScaleLoads; ++j) {
+        const int f = (wave * C::kScaleLoads + j) * 64 + lane;
+        sofs[j] = (uint32_t)(((f / C::kSB) * p.KB + kb0 + (f & (C::kSB - 1))) * 4);
+    }
+    // blocks whose piece `chunk` lies inside K: kb < kb_in
+    const int kb_in = (int)((K - chunk + kBlock - 1) / kBlock - kb0);
+    const int nkb = (int)KB;
+
+    // The fills of block kb named by `mask`: bit j weight piece j, bit 8 + j
+    // activation piece j, bit 16 the batch of scales that kb opens.  Blocks at
+    // or past the run's end are not loaded, but every wave issues the same
+    // number of loads (reading zero), so that the waits can count them.
+    auto issue = [&](char *stage, int kb, unsigned mask) __attribute__((always_inline)) {
+        const uint32_t kofs = (uint32_t)kb * kBlock;
+        if ((mask & 0x10000u) && (kb & (C::kSB - 1)) == 0) {
+            // (entries past the last block are the next row's, or zero: unused)
+#pragma unroll
+            for (int j = 0; j < C::kScaleLoads; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    sr, (BI8_LDS void *)&xsl[(kb / C::kSB) & 1][(wave * C::kScaleLoads + j) * 64], 4,
+                    sofs[j] + (uint32_t)kb * 4u, 0, 0, 0);
+        }
+        const bool in = kb < kb_in && kb < nkb;
+#pragma unroll
+        for (int j = 0; j < C::kWLoads; ++j)
+            if (mask & (1u << j))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (BI8_LDS void *)(stage + (wave + j * C::kWaves) * 1024),
+                                                         16, in ? go + kofs + j * piece_stride : kOobOffset, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < C::kXLoads; ++j)
+            if (mask & (0x100u << j))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    xr, (BI8_LDS void *)(stage + C::kXOff + (wave + j * C::kWaves) * 1024), 16,
+                    in ? go + kofs + j * piece_stride : kOobOffset, 0, 0, 0);
+    };
+
+    const int wn = wave % C::WN, wm = wave / C::WN;
+    const int rr = lane & 31, hi = lane >> 5;
+    const int swz = (rr & 7) ^ ((rr >> 3) & 1);
+    int frag_off[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) frag_off[s] = 16 * ((2 * s + hi) ^ swz);
+    const int wrow0 = (wn * C::kWaveN + rr) * 128;
+    const int xrow0 = C::kXOff + (wm * C::kWaveM + rr) * 128;
+    const int srow = (wm * C::kWaveM + rr) * C::kSB;
+
+    int64_t nbw = (t.n0 + wn * C::kWaveN) / kBlock;
+    if (nbw > p.NB - 1) nbw = p.NB - 1;
+    const BI8_CONST float *ws_row =
+        reinterpret_cast<const BI8_CONST float *>(reinterpret_cast<uintptr_t>(t.ws + nbw * p.KB + kb0));
+    float ws_cur = ws_row[0];
+
+    f32x16 zero16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero16[i] = 0.f;
+    f32x16 y[SA][SB];
+#pragma unroll
+    for (int a = 0; a < SA; ++a)
+#pragma unroll
+        for (int b = 0; b < SB; ++b) y[a][b] = zero16;
+
+    auto rescale = [&](const f32x16 &acc, f32x16 &yv, float tb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) yv[i] = fmaf(acc[i], tb, yv[i]);
+        // (a use here keeps the rescales from sinking past the next branch,
+        // which would keep every block sum live at once)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" ::"v"(yv[i]));
+    };
+
+    i32x4 xf[SB][4], wf0[4];
+    float xsv[SB], wsv;
+    auto read_first = [&](const char *stage, int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+            xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) wf0[s] = *reinterpret_cast<const i32x4 *>(stage + wrow0 + frag_off[s]);
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                xf[b][s] = *reinterpret_cast<const i32x4 *>(stage + xrow0 + b * 32 * 128 + frag_off[s]);
+        wsv = ws_cur;
+        ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
+    };
+    // Block kb is in LDS once this wave's fills of it have landed and every
+    // wave is past the barrier, which also ends every read of block kb - 1.
+    // Blocks kb + 1 .. kb + NS - 2 may still be in flight, with the batch of
+    // scales that one of them opens.
+    auto arrive = [&](int kb) __attribute__((always_inline)) {
+        if constexpr (NS == 2) {
+            wait_vmcnt<0>();
+        } else {
+            if ((kb & (C::kSB - 1)) >= C::kSB - (NS - 2))
+                wait_vmcnt<(NS - 2) * C::kLoads + C::kScaleLoads>();
+            else
+                wait_vmcnt<(NS - 2) * C::kLoads>();
+        }
+        lds_barrier();
+    };
+    // spread a block's fills over its first sub-tiles
+    constexpr int kSub = SA * SB;
+    constexpr int kSpread = kSub >= 8 ? 4 : kSub >= 2 ? 2 : 1;
+    auto fill_mask = [](int j) {
+        unsigned m = j == 0 ? 0x10000u : 0u;
+        for (int q = 0; q < C::kWLoads; ++q)
+            if (q % kSpread == j) m |= 1u << q;
+        for (int q = 0; q < C::kXLoads; ++q)
+            if (q % kSpread == j) m |= 0x100u << q;
+        return m;
+    };
+
+    // One K block: fills of block kb + NS - 1 into the stage of block kb - 1,
+    // the sub-tiles' MFMAs, each sub-tile's rescale behind the next one's.
+    auto compute = [&](const char *stage, char *ahead, const char *nxt, int kb) __attribute__((always_inline)) {
+        float tb[SB];
+#pragma unroll
+        for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
+        f32x16 acc[2];
+#pragma unroll
+        for (int a = 0; a < SA; ++a) {
+            i32x4 wf[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                wf[s] = a == 0 ? wf0[s]
+                               : *reinterpret_cast<const i32x4 *>(stage + wrow0 + a * 32 * 128 + frag_off[s]);
+#pragma unroll
+            for (int b = 0; b < SB; ++b) {
+                const int j = a * SB + b;
+                acc[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    join16(wf[0], wf[1]), join16(xf[b][0], xf[b][1]), zero16, 0, 0, 0, 0, 0, 0);
+                acc[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    join16(wf[2], wf[3]), join16(xf[b][2], xf[b][3]), acc[j & 1], 0, 0, 0, 0, 0, 0);
+                if (j < kSpread) issue(ahead, kb + NS - 1, fill_mask(j));
+                if (j > 0) rescale(acc[(j - 1) & 1], y[(j - 1) / SB][(j - 1) % SB], tb[(j - 1) % SB]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        asm volatile("" ::"v"(acc[(kSub - 1) & 1]));   // the last MFMAs stay ahead of the barrier
+        if (kb + 1 < nkb) {
+            arrive(kb + 1);
+            read_first(nxt, kb + 1);
+        }
+        rescale(acc[(kSub - 1) & 1], y[SA - 1][SB - 1], tb[SB - 1]);
+    };
+
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) issue(lds(i), i, 0x1FFFFu);
+    arrive(0);
+    read_first(lds0, 0);
+    for (int kb = 0; kb < nkb;) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            compute(lds(i), lds((i + NS - 1) % NS), lds((i + 1) % NS), kb);
+            if (++kb >= nkb) break;
+        }
+    }
+    wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
+
+    // Store.  32x32 result: lane -> token lane & 31; element i -> weight row
+    // 8 (i / 4) + 4 hi + i % 4.
+    if constexpr (SPLIT) {
+        bool whole = false;
+        float *rows;      // fp32 rows of this unit's partial sums, at tile row 0
+        int64_t pitch, ncols, nrows;
+        if constexpr (MOE) {
+            whole = t.split < 0;
+            rows = p.partial + t.unit * (int64_t)(C::kBM * C::kBN);
+            pitch = C::kBN;
+            ncols = C::kBN;
+            nrows = C::kBM;
+        } else {
+            rows = p.partial + (int64_t)blockIdx.y * p.M * p.N + t.m0 * p.N + t.n0;
+            pitch = p.N;
+            ncols = p.N - t.n0;
+            nrows = t.rows;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int b = 0; b < SB; ++b) {
+                const int64_t ml = wm * C::kWaveM + b * 32 + rr;
+                if (ml >= nrows) continue;
+#pragma unroll
+                for (int a = 0; a < SA; ++a)
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        const int64_t c = wn * C::kWaveN + a * 32 + 8 * i4 + 4 * hi;
+                        float *dst = rows + ml * pitch + c;
+                        if (MOE || p.wide_store) {
+                            if (c < ncols)
+                                *reinterpret_cast<f32x4 *>(dst) = f32x4{y[a][b][4 * i4], y[a][b][4 * i4 + 1],
+                                                                         y[a][b][4 * i4 + 2], y[a][b][4 * i4 + 3]};
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (c + e < ncols) dst[e] = y[a][b][4 * i4 + e];
+                        }
+                    }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+        const int64_t ml = wm * C::kWaveM + b * 32 + rr;
+        if (ml >= t.rows) continue;
+        uint16_t *yrow = p.y + (t.m0 + ml) * p.N;
+#pragma unroll
+        for (int a = 0; a < SA; ++a) {
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const int64_t n = t.n0 + wn * C::kWaveN + a * 32 + 8 * i4 + 4 * hi;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = y[a][b][4 * i4 + e];
+                    if (!MOE && p.bias && n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
+                }
+                if (p.wide_store) {
+                    if (n < p.N)
+                        *reinterpret_cast<uint2 *>(yrow + n) =
+                            make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N) yrow[n + e] = (uint16_t)(f32x2_to_bf16x2_bits(v[e], 0.0f) & 0xFFFFu);
+                }
+            }
+        }
+    }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+typedef Cfg<2, 4, 4, 2, 2> Cfg256x256;   // weight rows x activation rows
+typedef Cfg<4, 2, 2, 2, 3> Cfg256x128;
+typedef Cfg<4, 2, 1, 2, 4> Cfg128x128;
+typedef Cfg<4, 2, 1, 1, 4> Cfg128x64;
+
+// (the host pass has to emit the launch stubs)
+template __global__ void gemm_fp8_tiled_kernel<Cfg256x256, false, false, 4>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg256x256, true, false, 4>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, false, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, true, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, false, 8>(GemmArgs);
+
+template <class C, bool MOE, bool SPLIT, int64_t GM>
+hipError_t launch_tiled(GemmArgs p, hipStream_t stream, int64_t splits = 1) {
+    // grouped: at least the sum over experts of ceil(rows / BM) tiles
+    p.tiles_m = (p.M + C::kBM - 1) / C::kBM + (MOE ? p.E : 0);
+    p.tiles_n = (p.N + C::kBN - 1) / C::kBN;
+    const int64_t total = p.tiles_m * p.tiles_n + (MOE && SPLIT ? kTailRound : 0);
+    if (total > 0x7FFFFFFFll || splits < 1 || splits > 65535) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gemm_fp8_tiled_kernel<C, MOE, SPLIT, GM>), dim3((unsigned)total, (unsigned)splits),
+                       dim3(C::kThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <bool MOE>
+hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
+    switch (path) {
+        case Fp8Path::kSkinny: return launch_skinny<false, MOE>(p, MOE ? (p.M + p.E - 1) / p.E : p.M, stream);
+        case Fp8Path::kTile128x64: return launch_tiled<Cfg128x64, MOE, false, 8>(p, stream);
+        case Fp8Path::kTile128x128: return launch_tiled<Cfg128x128, MOE, false, 8>(p, stream);
+        case Fp8Path::kTile256x128: return launch_tiled<Cfg256x128, MOE, false, 8>(p, stream);
+        case Fp8Path::kTile256x256: return launch_tiled<Cfg256x256, MOE, false, 4>(p, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
 GemmArgs fp8_args(const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws, const uint16_t *bias,
                   uint16_t *y, int64_t M, int64_t N, int64_t K) {
     return make_args(reinterpret_cast<const int8_t *>(xq), xs, reinterpret_cast<const int8_t *>(w), ws, bias, y, M, N,
@@ -231,26 +596,41 @@ GemmArgs fp8_args(const uint8_t *xq, const float *xs, const uint8_t *w, const fl
 
 }  // namespace
 
+Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K) {
+    if (K % 16 != 0 || (M <= 64 && N * (16 + M) <= 360000)) return Fp8Path::kSkinny;
+    if (((M + 255) / 256) * ((N + 255) / 256) >= 256) return Fp8Path::kTile256x256;
+    if (((M + 127) / 128) * ((N + 255) / 256) >= 256) return Fp8Path::kTile256x128;
+    return Fp8Path::kTile128x64;
+}
+
+Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E) {
+    const int64_t mean = (R + E - 1) / E;
+    if (mean <= 32) return Fp8Path::kSkinny;
+    const int64_t wide_tiles = (int64_t)E * ((mean + 255) / 256) * ((N + 255) / 256);
+    return wide_tiles >= 1024 ? Fp8Path::kTile256x256 : Fp8Path::kTile256x128;
+}
+
 int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0; }
 
-hipError_t launch_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws, const uint16_t *bias,
-                           uint16_t *y, int64_t M, int64_t N, int64_t K, float *workspace, int64_t workspace_bytes,
-                           hipStream_t stream) {
+hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws,
+                           const uint16_t *bias, uint16_t *y, int64_t M, int64_t N, int64_t K, float *workspace,
+                           int64_t workspace_bytes, hipStream_t stream) {
     if (M == 0) return hipSuccess;
     const GemmArgs p = fp8_args(xq, xs, w, ws, bias, y, M, N, K);
-    return K % 16 != 0 ? launch_skinny<true, false>(p, M, stream) : launch_skinny<false, false>(p, M, stream);
+    if (K % 16 != 0) return launch_skinny<true, false>(p, M, stream);
+    return launch_path<false>(path == Fp8Path::kAuto ? select_gemm_fp8_path(M, N, K) : path, p, stream);
 }
 
 int64_t moe_gemm_fp8_workspace_bytes(int64_t R, int64_t N, int64_t K, int32_t E) { return 0; }
 
-hipError_t launch_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t *offsets, const uint8_t *w,
-                               const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K, int32_t E,
-                               float *workspace, int64_t workspace_bytes, hipStream_t stream) {
+hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const int32_t *offsets,
+                               const uint8_t *w, const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K,
+                               int32_t E, float *workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (R == 0) return hipSuccess;
     GemmArgs p = fp8_args(xq, xs, w, ws, nullptr, y, R, N, K);
     p.offsets = offsets;
     p.E = E;
-    return launch_skinny<false, true>(p, (R + E - 1) / E, stream);
+    return launch_path<true>(path == Fp8Path::kAuto ? select_moe_gemm_fp8_path(R, N, K, E) : path, p, stream);
 }
 
 }  // namespace bi8

@@ -12,9 +12,11 @@ import block_wise_int8_amd as _bi8
 from . import _call as c
 
 __all__ = ["quant_act_fp8", "quant_act_gather_fp8", "silu_mul_quant_fp8", "quant_weight_fp8", "gemm_fp8",
-           "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_fp8_workspace_size", "moe_layer_fp8"]
+           "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_fp8_workspace_size", "gemm_fp8_select",
+           "moe_gemm_fp8_select", "moe_layer_fp8", "GEMM_TILE_128X128"]
 
 FP8 = torch.float8_e4m3fn
+GEMM_TILE_128X128 = 5   # the kernel variant that the int8 GEMM does not have
 
 
 def declare(lib) -> None:
@@ -27,6 +29,10 @@ def declare(lib) -> None:
     c.declare(lib, "blockint8_gemm_fp8_workspace_size", [i64, i64, i64], i64)
     c.declare(lib, "blockint8_linear_fp8", [vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, i64, vp])
     c.declare(lib, "blockint8_moe_gemm_fp8", [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, vp])
+    c.declare(lib, "blockint8_gemm_fp8_variant", [i32] + lib.blockint8_gemm_fp8.argtypes)
+    c.declare(lib, "blockint8_moe_gemm_fp8_variant", [i32] + lib.blockint8_moe_gemm_fp8.argtypes)
+    c.declare(lib, "blockint8_gemm_fp8_select", [i64, i64, i64])
+    c.declare(lib, "blockint8_moe_gemm_fp8_select", [i64, i64, i64, i32])
     c.declare(lib, "blockint8_moe_gemm_fp8_workspace_size", [i64, i64, i64, i32], i64)
 
 
@@ -98,12 +104,14 @@ def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
 
 def gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
              bias: torch.Tensor | None = None, y: torch.Tensor | None = None,
-             workspace: torch.Tensor | None = None) -> torch.Tensor:
+             workspace: torch.Tensor | None = None, variant: int | None = None) -> torch.Tensor:
     """Block-scaled e4m3 GEMM ``y = x . W^T (+ bias)`` -> bf16 [M, N].
 
     ``workspace`` (any contiguous tensor on the device, of at least
     ``gemm_fp8_workspace_size`` bytes) lets problems with few tiles split K
-    between workgroups; calls that share one must not overlap in time."""
+    between workgroups; calls that share one must not overlap in time.
+    ``variant`` (one of ``GEMM_*``) runs a named kernel instead of the
+    shape-based choice."""
     dev = c.device_of(xq, "xq")
     c.dense(xq, "xq", dev, FP8, (None, None))
     M, K = xq.shape
@@ -115,8 +123,8 @@ def gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tens
         c.dense(bias, "bias", dev, torch.bfloat16, (N,))
     y = c.output(y, "y", dev, torch.bfloat16, (M, N))
     wsp, nbytes = c.scratch(workspace, dev)
-    _bi8._check(c.call(_bi8.load().blockint8_gemm_fp8, dev, xq.data_ptr(), xs.data_ptr(), w.data_ptr(), ws.data_ptr(),
-                       c.ptr(bias), y.data_ptr(), M, N, K, 128, 128, wsp, nbytes))
+    _bi8._check(c.call(_bi8.load().blockint8_gemm_fp8_variant, dev, variant or 0, xq.data_ptr(), xs.data_ptr(),
+                       w.data_ptr(), ws.data_ptr(), c.ptr(bias), y.data_ptr(), M, N, K, 128, 128, wsp, nbytes))
     return y
 
 
@@ -144,20 +152,30 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, bias: torch.T
     return y
 
 
+def gemm_fp8_select(M: int, N: int, K: int) -> int:
+    """The kernel variant (``GEMM_*``) that ``gemm_fp8`` runs for this shape."""
+    return int(_bi8.load().blockint8_gemm_fp8_select(M, N, K))
+
+
+def moe_gemm_fp8_select(R: int, N: int, K: int, E: int) -> int:
+    """The kernel variant (``GEMM_*``) that ``moe_gemm_fp8`` runs for this shape."""
+    return int(_bi8.load().blockint8_moe_gemm_fp8_select(R, N, K, E))
+
+
 def moe_gemm_fp8_workspace_size(R: int, N: int, K: int, E: int) -> int:
     """Bytes of workspace ``moe_gemm_fp8`` can use for the grouped problem (0: none)."""
     return int(_bi8.load().blockint8_moe_gemm_fp8_workspace_size(R, N, K, E))
 
 
 def moe_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Tensor,
-                 ws: torch.Tensor, y: torch.Tensor | None = None,
-                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+                 ws: torch.Tensor, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 variant: int | None = None) -> torch.Tensor:
     """Grouped block-scaled e4m3 GEMM over expert-sorted rows -> bf16 [R, N].
 
     ``expert_offsets`` is int32 [E+1] on the device (rows [off[e], off[e+1])
     use expert e); ``w`` is float8_e4m3fn [E, N, K], ``ws`` float32 [E,
-    ceil(N/128), ceil(K/128)].  ``workspace`` as for gemm_fp8, of
-    ``moe_gemm_fp8_workspace_size`` bytes."""
+    ceil(N/128), ceil(K/128)].  ``workspace`` and ``variant`` as for gemm_fp8,
+    with ``moe_gemm_fp8_workspace_size`` bytes."""
     dev = c.device_of(xq, "xq")
     c.dense(xq, "xq", dev, FP8, (None, None))
     R, K = xq.shape
@@ -168,7 +186,7 @@ def moe_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: torch.Tenso
     c.dense(ws, "ws", dev, torch.float32, (E, _blocks(N), _blocks(K)))
     y = c.output(y, "y", dev, torch.bfloat16, (R, N))
     wsp, nbytes = c.scratch(workspace, dev)
-    _bi8._check(c.call(_bi8.load().blockint8_moe_gemm_fp8, dev, xq.data_ptr(), xs.data_ptr(),
+    _bi8._check(c.call(_bi8.load().blockint8_moe_gemm_fp8_variant, dev, variant or 0, xq.data_ptr(), xs.data_ptr(),
                        expert_offsets.data_ptr(), w.data_ptr(), ws.data_ptr(), y.data_ptr(), R, N, K, E, 128, 128, wsp,
                        nbytes))
     return y

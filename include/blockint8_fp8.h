@@ -141,6 +141,30 @@ int32_t blockint8_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t
 
 int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, int32_t E);
 
+/*
+ * Kernel variants, as in blockint8.h: the *_select functions tell which kernel
+ * blockint8_gemm_fp8 / blockint8_moe_gemm_fp8 choose for a size, the *_variant
+ * forms run a named one, with the same arguments, results and errors.  Every
+ * variant runs every size with K % 16 == 0, dense and grouped; with K % 16 != 0
+ * only BI8_GEMM_AUTO is accepted (BI8_ERR_ALIGN otherwise).  An unknown variant
+ * is BI8_ERR_SHAPE.  The ids are those of blockint8.h and one more.
+ */
+enum { BI8_GEMM_TILE_128X128 = 5 };
+
+int32_t blockint8_gemm_fp8_select(int64_t M, int64_t N, int64_t K);
+
+int32_t blockint8_moe_gemm_fp8_select(int64_t R, int64_t N, int64_t K, int32_t E);
+
+int32_t blockint8_gemm_fp8_variant(int32_t variant, const uint8_t *xq, const float *xs, const uint8_t *w,
+                                   const float *ws, const uint16_t *bias, uint16_t *y, int64_t M, int64_t N, int64_t K,
+                                   int32_t block_n, int32_t block_k, void *workspace, int64_t workspace_bytes,
+                                   void *stream);
+
+int32_t blockint8_moe_gemm_fp8_variant(int32_t variant, const uint8_t *xq, const float *xs,
+                                       const int32_t *expert_offsets, const uint8_t *w, const float *ws, uint16_t *y,
+                                       int64_t R, int64_t N, int64_t K, int32_t E, int32_t block_n, int32_t block_k,
+                                       void *workspace, int64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -106,6 +106,17 @@ def test_every_declared_function_is_exported(header):
     assert wanted <= names
 
 
+def test_variant_rules():
+    lib, a = bi8.load(), list(CALLS["gemm_fp8"].values())
+    assert lib.blockint8_gemm_fp8_variant(6, *a, None) == SHAPE
+    assert lib.blockint8_gemm_fp8_variant(-1, *a, None) == SHAPE
+    a[list(CALLS["gemm_fp8"]).index("K")] = 250
+    assert lib.blockint8_gemm_fp8_variant(3, *a, None) == ALIGN
+    assert lib.blockint8_moe_gemm_fp8_variant(6, *CALLS["moe_gemm_fp8"].values(), None) == SHAPE
+    for M, N, K in [(1, 4096, 4096), (64, 8192, 4096), (333, 5000, 4000), (4096, 4096, 4096), (2048, 28672, 4096)]:
+        assert 1 <= bi8.gemm_fp8_select(M, N, K) <= 5 and 1 <= bi8.moe_gemm_fp8_select(M, N, K, 8) <= 5
+
+
 def test_workspace_sizes_of_bad_problems_are_zero():
     assert bi8.gemm_fp8_workspace_size(0, 10, 10) == 0 and bi8.gemm_fp8_workspace_size(10, -1, 10) == 0
     assert bi8.moe_gemm_fp8_workspace_size(8, 10, 100, 2) == 0 and bi8.moe_gemm_fp8_workspace_size(8, 10, 128, 0) == 0

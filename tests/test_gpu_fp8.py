@@ -194,6 +194,38 @@ def test_gemm_with_a_workspace(M, N, K):
         assert torch.equal(short.view(torch.int16), run_gemm(*c).view(torch.int16))
 
 
+VARIANTS = [bi8.GEMM_SKINNY, bi8.GEMM_TILE_128X64, bi8.GEMM_TILE_128X128, bi8.GEMM_TILE_256X128,
+            bi8.GEMM_TILE_256X256]
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (3, 260, 112), (65, 129, 128), (130, 300, 272), (257, 515, 1040),
+                                   (520, 700, 144), (300, 1030, 2320), (17, 40, 1168)])
+def test_every_variant(M, N, K, variant):
+    c = product_case((68, M, N, K), M, N, K, True)
+    y = bi8.gemm_fp8(codes_dev(c[0]), to_dev(c[1]), codes_dev(c[2]), to_dev(c[3]), bf16_to_dev(c[4]), variant=variant)
+    check_product(y, *fp8.gemm_f64(*c), K)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_every_variant_keeps_nan_codes_in_place(variant):
+    M, N, K = 300, 290, 400   # K ends inside a block
+    xq, xs, w, ws, _ = product_case((69, M, N, K), M, N, K, False)
+    xq[7, K - 1], xq[299, 0], w[11, K - 1], w[289, 0] = 0x7F, 0xFF, 0x7F, 0x7F
+    y = bi8.gemm_fp8(codes_dev(xq), to_dev(xs), codes_dev(w), to_dev(ws), variant=variant).float().cpu().numpy()
+    bad = np.zeros((M, N), bool)
+    bad[[7, 299]], bad[:, [11, 289]] = True, True
+    assert np.array_equal(np.isnan(y), bad)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 9000), (300, 260, 66000)])
+def test_long_k(M, N, K):
+    c = product_case((70, M, N, K), M, N, K, False)
+    for variant in [None] + (VARIANTS if K % 16 == 0 else []):
+        y = bi8.gemm_fp8(codes_dev(c[0]), to_dev(c[1]), codes_dev(c[2]), to_dev(c[3]), variant=variant)
+        check_product(y, *fp8.gemm_f64(*c), K, variant)
+
+
 def test_gemm_exact_integers():
     """Small whole codes and power-of-two scales: every sum is exact in binary32, and no product of a run
     lies 2^-13 below another."""
@@ -278,6 +310,14 @@ def test_moe_gemm(segments, N, K):
     first = run_grouped(*c, workspace=wsp)
     check_product(first, *ref, K, "workspace")
     assert torch.equal(first.view(torch.int16), run_grouped(*c, workspace=wsp).view(torch.int16))
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("segments,N,K", [([0, 3, 0, 5, 0], 130, 272), ([130, 7, 260, 0, 33], 640, 272),
+                                          ([300, 1, 513], 520, 1168), ([1] * 40, 64, 144)])
+def test_moe_every_variant(segments, N, K, variant):
+    c = grouped_case((74, N, K), segments, N, K)
+    check_product(run_grouped(*c, variant=variant), *fp8.moe_gemm_f64(*c), K)
 
 
 def test_moe_gemm_rows_past_the_last_segment_stay():
