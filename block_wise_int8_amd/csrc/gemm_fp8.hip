@@ -260,8 +260,53 @@ struct Cfg {
     static_assert(128 % kWaveN == 0, "a wave's weight rows lie in one scale block");
     static_assert(kScaleLoads >= 1 && kBM * kSB % (64 * kWaves) == 0, "scale split");
     static_assert(kWaves % 2 == 0, "a lane's pieces share their parity");
-    static_assert(NS >= 2 && NS <= 4 && NS - 2 < kSB, "ring depth");
+    static_assert(NS >= 3 && NS <= 4 && NS - 2 < kSB, "ring depth");
 };
+
+// Store a wave's SA x SB sub-tiles as bf16, the bias added: weight rows from n0,
+// tile rows from ml0 of the tile at row m0 with `rows` valid rows.  32x32
+// result: lane -> token lane & 31; element i -> weight row 8 (i / 4) + 4 (lane /
+// 32) + i % 4.
+template <int SA, int SB>
+__device__ __forceinline__ void store_tile(const GemmArgs &p, const f32x16 (&y)[SA][SB], int64_t n0, int64_t m0,
+                                           int64_t rows, int ml0, int lane) {
+    const int rr = lane & 31, hi = lane >> 5;
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+        const int64_t ml = ml0 + b * 32 + rr;
+        if (ml >= rows) continue;
+        uint16_t *yrow = p.y + (m0 + ml) * p.N;
+#pragma unroll
+        for (int a = 0; a < SA; ++a) {
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                const int64_t n = n0 + a * 32 + 8 * i4 + 4 * hi;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = y[a][b][4 * i4 + e];
+                    if (p.bias && n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
+                }
+                if (p.wide_store) {
+                    if (n < p.N)
+                        *reinterpret_cast<uint2 *>(yrow + n) =
+                            make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N) yrow[n + e] = (uint16_t)(f32x2_to_bf16x2_bits(v[e], 0.0f) & 0xFFFFu);
+                }
+            }
+        }
+    }
+}
+
+// Wait until at most N buffer-to-LDS fills are in flight (63: any number) and
+// every LDS read has returned.
+template <int N>
+__device__ __forceinline__ void wait_lds() {
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
+}
 
 // SPLIT: a workgroup sums only a run of K blocks and stores fp32 partial sums:
 // dense, run blockIdx.y of kb_per_split blocks, in p.partial[blockIdx.y];
@@ -518,51 +563,278 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
             return;
         }
     }
-#pragma unroll
-    for (int b = 0; b < SB; ++b) {
-        const int64_t ml = wm * C::kWaveM + b * 32 + rr;
-        if (ml >= t.rows) continue;
-        uint16_t *yrow = p.y + (t.m0 + ml) * p.N;
-#pragma unroll
-        for (int a = 0; a < SA; ++a) {
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-                const int64_t n = t.n0 + wn * C::kWaveN + a * 32 + 8 * i4 + 4 * hi;
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = y[a][b][4 * i4 + e];
-                    if (!MOE && p.bias && n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
-                }
-                if (p.wide_store) {
-                    if (n < p.N)
-                        *reinterpret_cast<uint2 *>(yrow + n) =
-                            make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < p.N) yrow[n + e] = (uint16_t)(f32x2_to_bf16x2_bits(v[e], 0.0f) & 0xFFFFu);
-                }
-            }
-        }
-    }
+    store_tile<SA, SB>(p, y, t.n0 + wn * C::kWaveN, t.m0, t.rows, wm * C::kWaveM, lane);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-typedef Cfg<2, 4, 4, 2, 2> Cfg256x256;   // weight rows x activation rows
-typedef Cfg<4, 2, 2, 2, 3> Cfg256x128;
+// ---------------------------------------------------------------------------
+// Ping-pong path: 256 x 256 tile
+// ---------------------------------------------------------------------------
+//
+// Eight waves of 128 weight rows x 64 activation rows.  Waves w and w + 4 share
+// a SIMD and belong to two groups that run half a step apart: between two
+// barriers one group issues the four MFMAs of a cluster (one 32-row weight
+// sub-row against its two 32-row activation sub-rows), the other reads the
+// fragments of its next cluster, issues fills and rescales its previous
+// cluster.  A K block is four clusters, eight barriers.
+//
+// The two stages of 64 KB are refilled piecewise: the activation rows of block
+// kb + 2 as soon as both groups have read those of kb into registers, the
+// weight sub-rows a cluster or two after they were read, so that fills run
+// between one and two blocks ahead and no wait drains them.
+//
+// The fills are written out as instructions: a region is refilled while the
+// other half of its stage is read, in an order that the waits below count, and
+// the compiler's own tracking would drain every fill at each block.  They have
+// no result register; the memory clobber keeps LDS reads on their side.
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)(uintptr_t)(const BI8_LDS void *)p;
+}
+__device__ __forceinline__ void fill16(i32x4 rsrc, uint32_t lds, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
+}
+__device__ __forceinline__ void fill4(i32x4 rsrc, uint32_t lds, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
+}
+// The words of make_rsrc's buffer resource, wave-uniform.
+__device__ __forceinline__ i32x4 rsrc_words(const void *base, uint32_t num_bytes) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(base);
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF);
+    r[2] = __builtin_amdgcn_readfirstlane((int)num_bytes);
+    r[3] = 0x00020000;
+    return r;
+}
+
+struct PingPong {
+    static constexpr int kThreads = 512;
+    static constexpr int kBN = 256, kBM = 256, SA = 4, SB = 2;
+    static constexpr int kSB = 8;
+    static constexpr int kScaleLoads = kBM * kSB / 64 / 8;
+};
+
+template <bool MOE, int64_t GM>
+__global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using C = PingPong;
+    constexpr int SA = C::SA, SB = C::SB;
+    __shared__ __attribute__((aligned(1024))) char x0[C::kBM * 128];
+    __shared__ __attribute__((aligned(1024))) char x1[C::kBM * 128];
+    __shared__ __attribute__((aligned(1024))) char w0[C::kBN * 128];   // row 128 g + 32 a + i of the tile: group g,
+    __shared__ __attribute__((aligned(1024))) char w1[C::kBN * 128];   // sub-row a
+    __shared__ float xsl[2][C::kBM * C::kSB];
+
+    Tile t;
+    if (!decode_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
+    if (t.rows <= 0) return;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave >> 2, wm = wave & 3;
+    const int64_t K = p.K;
+    const int nkb = (int)p.KB;
+
+    const int64_t wrows = p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN;
+    const i32x4 wr = rsrc_words(t.w + t.n0 * K, clamp_bytes(wrows * K));
+    const i32x4 xr = rsrc_words(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
+    const i32x4 sr = rsrc_words(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
+
+    // Pieces of 1 KB as in the tiled kernel.  A wave fills, of weight sub-row a,
+    // rows 128 wn + 32 a + 8 wm + [0, 8), and activation rows 8 (wave + 8 j).
+    const int r_in = lane >> 3;
+    const int chunk = 16 * ((lane & 7) ^ r_in ^ (wave & 1));
+    const uint32_t wgo = (uint32_t)((128 * wn + 8 * wm + r_in) * K + chunk);
+    const uint32_t xgo = (uint32_t)((8 * wave + r_in) * K + chunk);
+    const uint32_t wstride = (uint32_t)(32 * K), xstride = (uint32_t)(64 * K);
+    const int kb_in = (int)((K - chunk + kBlock - 1) / kBlock);
+    const uint32_t wlds[2] = {lds_address(w0) + wn * 16384 + wm * 1024, lds_address(w1) + wn * 16384 + wm * 1024};
+    const uint32_t xlds[2] = {lds_address(x0) + wave * 1024, lds_address(x1) + wave * 1024};
+    const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
+    // (st: the stage, kb & 1)
+    auto fill_w = [&](const int st, const int a, int kb) __attribute__((always_inline)) {
+        fill16(wr, wlds[st] + a * 4096, kb < kb_in ? wgo + a * wstride + (uint32_t)kb * kBlock : kOobOffset);
+    };
+    auto fill_x = [&](const int st, const int j, int kb) __attribute__((always_inline)) {
+        fill16(xr, xlds[st] + j * 8192, kb < kb_in ? xgo + j * xstride + (uint32_t)kb * kBlock : kOobOffset);
+    };
+    // Entry (row, block) of a batch at row * kSB + block; entries past the last
+    // block are the next row's, or zero: unused.
+    auto fill_scales = [&](int kb) __attribute__((always_inline)) {
+        const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
+        const int f = wave * C::kScaleLoads * 64 + lane;
+        const uint32_t off = (uint32_t)(((f / C::kSB) * p.KB + kb + (f & (C::kSB - 1))) * 4);
+#pragma unroll
+        for (int j = 0; j < C::kScaleLoads; ++j) fill4(sr, dst + j * 256, off + (uint32_t)(j * 8 * 4 * p.KB));
+    };
+
+    const int rr = lane & 31, hi = lane >> 5;
+    const int swz = (rr & 7) ^ ((rr >> 3) & 1);
+    int frag_off[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) frag_off[s] = 16 * ((2 * s + hi) ^ swz);
+    const int wrow0 = (wn * 128 + rr) * 128;
+    const int xrow0 = (wm * 64 + rr) * 128;
+    const int srow = (wm * 64 + rr) * C::kSB;
+
+    int64_t nbw = t.n0 / kBlock + wn;
+    if (nbw > p.NB - 1) nbw = p.NB - 1;
+    const BI8_CONST float *ws_row =
+        reinterpret_cast<const BI8_CONST float *>(reinterpret_cast<uintptr_t>(t.ws + nbw * p.KB));
+    float ws_cur = ws_row[0];
+
+    f32x16 zero16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero16[i] = 0.f;
+    f32x16 y[SA][SB], acc[SB];
+    float tb[SB], xsv[SB], wsv = 0.f;
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+        acc[b] = zero16;
+        tb[b] = 0.f;
+#pragma unroll
+        for (int a = 0; a < SA; ++a) y[a][b] = zero16;
+    }
+    i32x4 xf[SB][4], wf[4];
+
+    auto rescale = [&](auto ac) __attribute__((always_inline)) {
+        constexpr int a = decltype(ac)::value;
+#pragma unroll
+        for (int b = 0; b < SB; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[a][b][i] = fmaf(acc[b][i], tb[b], y[a][b][i]);
+        }
+#pragma unroll
+        for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(y[a][b]));
+    };
+    // Memory phase of cluster a of block kb, in stage st.  Fills, in this order
+    // from block to block:
+    //   a = 1: activation pieces 0, 1 of kb + 2    a = 2: pieces 2, 3
+    //   a = 3: weight sub-rows 0, 1 of kb + 2      a = 0: sub-rows 2, 3 of kb + 1
+    // The waits leave the younger fills in flight (a batch of scales among
+    // them only makes a wait stricter).
+    auto memory = [&](auto ac, auto sc, int kb) __attribute__((always_inline)) {
+        constexpr int a = decltype(ac)::value, st = decltype(sc)::value;
+        const char *w = (st ? w1 : w0) + wrow0 + a * 4096;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) wf[s] = *reinterpret_cast<const i32x4 *>(w + frag_off[s]);
+        if constexpr (a == 0) {
+            const char *x = (st ? x1 : x0) + xrow0;
+#pragma unroll
+            for (int b = 0; b < SB; ++b)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) xf[b][s] = *reinterpret_cast<const i32x4 *>(x + b * 4096 + frag_off[s]);
+#pragma unroll
+            for (int b = 0; b < SB; ++b)
+                xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+            wsv = ws_cur;
+            ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
+            if (((kb + 2) & (C::kSB - 1)) == 0) fill_scales(kb + 2);
+            fill_w(st ^ 1, 2, kb + 1);
+            fill_w(st ^ 1, 3, kb + 1);
+        } else if constexpr (a == 1) {
+            fill_x(st, 0, kb + 2);
+            fill_x(st, 1, kb + 2);
+        } else if constexpr (a == 2) {
+            fill_x(st, 2, kb + 2);
+            fill_x(st, 3, kb + 2);
+        } else {
+            fill_w(st, 0, kb + 2);
+            fill_w(st, 1, kb + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        rescale(std::integral_constant<int, (a + 3) % 4>{});
+        if constexpr (a == 1)
+            wait_lds<10>();   // weight sub-rows 2, 3 of this block are in
+        else if constexpr (a == 3)
+            wait_lds<8>();    // the activation rows and sub-rows 0, 1 of the next block
+        else
+            wait_lds<63>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto math = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+            acc[b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[b][0], xf[b][1]),
+                                                                     zero16, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+            acc[b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[b][2], xf[b][3]),
+                                                                     acc[b], 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(acc[b]));
+    };
+    auto cluster = [&](auto ac, auto sc, int kb) __attribute__((always_inline)) {
+        memory(ac, sc, kb);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        math();
+        if constexpr (decltype(ac)::value == 0) {
+#pragma unroll
+            for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto block = [&](auto sc, int kb) __attribute__((always_inline)) {
+        cluster(std::integral_constant<int, 0>{}, sc, kb);
+        cluster(std::integral_constant<int, 1>{}, sc, kb);
+        cluster(std::integral_constant<int, 2>{}, sc, kb);
+        cluster(std::integral_constant<int, 3>{}, sc, kb);
+    };
+    fill_scales(0);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fill_x(st, j, st);
+#pragma unroll
+        for (int a = 0; a < (st ? 2 : 4); ++a) fill_w(st, a, st);
+    }
+    wait_lds<8>();
+    lds_barrier();
+    if (wn == 1) lds_barrier();   // group 1 runs one phase behind
+    for (int kb = 0;;) {
+        block(std::integral_constant<int, 0>{}, kb);
+        if (++kb >= nkb) break;
+        block(std::integral_constant<int, 1>{}, kb);
+        if (++kb >= nkb) break;
+    }
+    if (wn == 0) lds_barrier();
+    rescale(std::integral_constant<int, 3>{});
+    wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
+
+    store_tile<SA, SB>(p, y, t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+typedef Cfg<4, 2, 2, 2, 3> Cfg256x128;   // weight rows x activation rows
 typedef Cfg<4, 2, 1, 2, 4> Cfg128x128;
 typedef Cfg<4, 2, 1, 1, 4> Cfg128x64;
 
 // (the host pass has to emit the launch stubs)
-template __global__ void gemm_fp8_tiled_kernel<Cfg256x256, false, false, 4>(GemmArgs);
-template __global__ void gemm_fp8_tiled_kernel<Cfg256x256, true, false, 4>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, true, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, false, 8>(GemmArgs);
+
+template __global__ void gemm_fp8_pingpong_kernel<false, 4>(GemmArgs);
+template __global__ void gemm_fp8_pingpong_kernel<true, 4>(GemmArgs);
+
+template <bool MOE, int64_t GM>
+hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
+    p.tiles_m = (p.M + 255) / 256 + (MOE ? p.E : 0);
+    p.tiles_n = (p.N + 255) / 256;
+    const int64_t total = p.tiles_m * p.tiles_n;
+    if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gemm_fp8_pingpong_kernel<MOE, GM>), dim3((unsigned)total), dim3(PingPong::kThreads), 0, stream,
+                       p);
+    return hipGetLastError();
+}
 
 template <class C, bool MOE, bool SPLIT, int64_t GM>
 hipError_t launch_tiled(GemmArgs p, hipStream_t stream, int64_t splits = 1) {
@@ -583,7 +855,7 @@ hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
         case Fp8Path::kTile128x64: return launch_tiled<Cfg128x64, MOE, false, 8>(p, stream);
         case Fp8Path::kTile128x128: return launch_tiled<Cfg128x128, MOE, false, 8>(p, stream);
         case Fp8Path::kTile256x128: return launch_tiled<Cfg256x128, MOE, false, 8>(p, stream);
-        case Fp8Path::kTile256x256: return launch_tiled<Cfg256x256, MOE, false, 4>(p, stream);
+        case Fp8Path::kTile256x256: return launch_pingpong<MOE, 4>(p, stream);
         default: return hipErrorInvalidValue;
     }
 }
