@@ -590,13 +590,14 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return (uint32_t)(uintptr_t)(const BI8_LDS void *)p;
 }
-__device__ __forceinline__ void fill16(i32x4 rsrc, uint32_t lds, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
+// (the range check covers off + soff, and knows no wrap)
+__device__ __forceinline__ void fill16(i32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory", "m0");
 }
-__device__ __forceinline__ void fill4(i32x4 rsrc, uint32_t lds, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
+__device__ __forceinline__ void fill4(i32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory", "m0");
 }
 // The words of make_rsrc's buffer resource, wave-uniform.
 __device__ __forceinline__ i32x4 rsrc_words(const void *base, uint32_t num_bytes) {
@@ -621,10 +622,10 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = PingPong;
     constexpr int SA = C::SA, SB = C::SB;
-    __shared__ __attribute__((aligned(1024))) char x0[C::kBM * 128];
-    __shared__ __attribute__((aligned(1024))) char x1[C::kBM * 128];
-    __shared__ __attribute__((aligned(1024))) char w0[C::kBN * 128];   // row 128 g + 32 a + i of the tile: group g,
-    __shared__ __attribute__((aligned(1024))) char w1[C::kBN * 128];   // sub-row a
+    // weight stages 0, 1 (row 128 g + 32 a + i: group g, sub-row a), then
+    // activation stages 0, 1
+    constexpr int kStage = 32768, kX = 2 * kStage;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kStage];
     __shared__ float xsl[2][C::kBM * C::kSB];
 
     Tile t;
@@ -650,33 +651,42 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     const uint32_t xgo = (uint32_t)((8 * wave + r_in) * K + chunk);
     const uint32_t wstride = (uint32_t)(32 * K), xstride = (uint32_t)(64 * K);
     const int kb_in = (int)((K - chunk + kBlock - 1) / kBlock);
-    const uint32_t wlds[2] = {lds_address(w0) + wn * 16384 + wm * 1024, lds_address(w1) + wn * 16384 + wm * 1024};
-    const uint32_t xlds[2] = {lds_address(x0) + wave * 1024, lds_address(x1) + wave * 1024};
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t wlds = lds0 + wn * 16384 + wm * 1024, xlds = lds0 + kX + wave * 1024;
     const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
-    // (st: the stage, kb & 1)
+    // the lane's offsets, out of range in blocks where its piece lies past K
+    uint32_t wv = wgo, xv = xgo;
+    auto aim = [&](int kb) __attribute__((always_inline)) {
+        wv = kb < kb_in ? wgo : kOobOffset;
+        xv = kb < kb_in ? xgo : kOobOffset;
+    };
+    // (st: the stage, kb & 1; wv and xv aimed at kb)
     auto fill_w = [&](const int st, const int a, int kb) __attribute__((always_inline)) {
-        fill16(wr, wlds[st] + a * 4096, kb < kb_in ? wgo + a * wstride + (uint32_t)kb * kBlock : kOobOffset);
+        fill16(wr, wlds + st * kStage + a * 4096, wv, a * wstride + (uint32_t)kb * kBlock);
     };
     auto fill_x = [&](const int st, const int j, int kb) __attribute__((always_inline)) {
-        fill16(xr, xlds[st] + j * 8192, kb < kb_in ? xgo + j * xstride + (uint32_t)kb * kBlock : kOobOffset);
+        fill16(xr, xlds + st * kStage + j * 8192, xv, j * xstride + (uint32_t)kb * kBlock);
     };
     // Entry (row, block) of a batch at row * kSB + block; entries past the last
     // block are the next row's, or zero: unused.
     auto fill_scales = [&](int kb) __attribute__((always_inline)) {
         const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
         const int f = wave * C::kScaleLoads * 64 + lane;
-        const uint32_t off = (uint32_t)(((f / C::kSB) * p.KB + kb + (f & (C::kSB - 1))) * 4);
+        const uint32_t off = (uint32_t)(((f / C::kSB) * p.KB + (f & (C::kSB - 1))) * 4);
 #pragma unroll
-        for (int j = 0; j < C::kScaleLoads; ++j) fill4(sr, dst + j * 256, off + (uint32_t)(j * 8 * 4 * p.KB));
+        for (int j = 0; j < C::kScaleLoads; ++j)
+            fill4(sr, dst + j * 256, off, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
     };
 
     const int rr = lane & 31, hi = lane >> 5;
     const int swz = (rr & 7) ^ ((rr >> 3) & 1);
-    int frag_off[4];
+    int wfrag[4], xfrag[4];   // fragment addresses of sub-row 0, stage 0
 #pragma unroll
-    for (int s = 0; s < 4; ++s) frag_off[s] = 16 * ((2 * s + hi) ^ swz);
-    const int wrow0 = (wn * 128 + rr) * 128;
-    const int xrow0 = (wm * 64 + rr) * 128;
+    for (int s = 0; s < 4; ++s) {
+        const int piece = 16 * ((2 * s + hi) ^ swz);
+        wfrag[s] = (wn * 128 + rr) * 128 + piece;
+        xfrag[s] = kX + (wm * 64 + rr) * 128 + piece;
+    }
     const int srow = (wm * 64 + rr) * C::kSB;
 
     int64_t nbw = t.n0 / kBlock + wn;
@@ -699,15 +709,12 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     }
     i32x4 xf[SB][4], wf[4];
 
-    auto rescale = [&](auto ac) __attribute__((always_inline)) {
-        constexpr int a = decltype(ac)::value;
+    // elements [i0, i0 + n) of sub-tile (a, b)
+    auto rescale = [&](const int a, const int b, const int i0, const int n) __attribute__((always_inline)) {
 #pragma unroll
-        for (int b = 0; b < SB; ++b) {
+        for (int i = i0; i < i0 + n; ++i) y[a][b][i] = fmaf(acc[b][i], tb[b], y[a][b][i]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[a][b][i] = fmaf(acc[b][i], tb[b], y[a][b][i]);
-        }
-#pragma unroll
-        for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(y[a][b]));
+        for (int i = i0; i < i0 + n; ++i) asm volatile("" ::"v"(y[a][b][i]));
     };
     // Memory phase of cluster a of block kb, in stage st.  Fills, in this order
     // from block to block:
@@ -717,15 +724,14 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     // them only makes a wait stricter).
     auto memory = [&](auto ac, auto sc, int kb) __attribute__((always_inline)) {
         constexpr int a = decltype(ac)::value, st = decltype(sc)::value;
-        const char *w = (st ? w1 : w0) + wrow0 + a * 4096;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) wf[s] = *reinterpret_cast<const i32x4 *>(w + frag_off[s]);
+        for (int s = 0; s < 4; ++s) wf[s] = *reinterpret_cast<const i32x4 *>(lds + wfrag[s] + (st * kStage + a * 4096));
         if constexpr (a == 0) {
-            const char *x = (st ? x1 : x0) + xrow0;
 #pragma unroll
             for (int b = 0; b < SB; ++b)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) xf[b][s] = *reinterpret_cast<const i32x4 *>(x + b * 4096 + frag_off[s]);
+                for (int s = 0; s < 4; ++s)
+                    xf[b][s] = *reinterpret_cast<const i32x4 *>(lds + xfrag[s] + (st * kStage + b * 4096));
 #pragma unroll
             for (int b = 0; b < SB; ++b)
                 xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
@@ -735,6 +741,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
             fill_w(st ^ 1, 2, kb + 1);
             fill_w(st ^ 1, 3, kb + 1);
         } else if constexpr (a == 1) {
+            aim(kb + 2);
             fill_x(st, 0, kb + 2);
             fill_x(st, 1, kb + 2);
         } else if constexpr (a == 2) {
@@ -745,7 +752,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
             fill_w(st, 1, kb + 2);
         }
         __builtin_amdgcn_sched_barrier(0);
-        rescale(std::integral_constant<int, (a + 3) % 4>{});
+        rescale((a + 3) % 4, 0, 0, 16);
         if constexpr (a == 1)
             wait_lds<10>();   // weight sub-rows 2, 3 of this block are in
         else if constexpr (a == 3)
@@ -754,15 +761,30 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
             wait_lds<63>();
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto math = [&]() __attribute__((always_inline)) {
+    // Math phase: the cluster's MFMAs, and between them the rescale of the
+    // previous cluster's second sub-tile (that of the first runs in the memory
+    // phase): each wave's vector work is spread over both phases, and neither
+    // waits for an MFMA that has just been issued.
+    auto math = [&](auto ac) __attribute__((always_inline)) {
+        constexpr int a = decltype(ac)::value, before = (a + 3) % 4;
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[0][0], xf[0][1]),
+                                                                 zero16, 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        rescale(before, 1, 0, 8);
+        __builtin_amdgcn_sched_barrier(0);
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[0][2], xf[0][3]),
+                                                                 acc[0], 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        rescale(before, 1, 8, 8);
+        if constexpr (a == 0) {
 #pragma unroll
-        for (int b = 0; b < SB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[b][0], xf[b][1]),
-                                                                     zero16, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-        for (int b = 0; b < SB; ++b)
-            acc[b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[b][2], xf[b][3]),
-                                                                     acc[b], 0, 0, 0, 0, 0, 0);
+            for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[1][0], xf[1][1]),
+                                                                 zero16, 0, 0, 0, 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[1][2], xf[1][3]),
+                                                                 acc[1], 0, 0, 0, 0, 0, 0);
 #pragma unroll
         for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(acc[b]));
     };
@@ -770,11 +792,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
         memory(ac, sc, kb);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        math();
-        if constexpr (decltype(ac)::value == 0) {
-#pragma unroll
-            for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
-        }
+        math(ac);
         __builtin_amdgcn_sched_barrier(0);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -788,6 +806,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     fill_scales(0);
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
+        aim(st);
 #pragma unroll
         for (int j = 0; j < 4; ++j) fill_x(st, j, st);
 #pragma unroll
@@ -803,7 +822,8 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
         if (++kb >= nkb) break;
     }
     if (wn == 0) lds_barrier();
-    rescale(std::integral_constant<int, 3>{});
+    rescale(3, 0, 0, 16);
+    rescale(3, 1, 0, 16);
     wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
 
     store_tile<SA, SB>(p, y, t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
