@@ -267,8 +267,8 @@ struct Cfg {
 // tile rows from ml0 of the tile at row m0 with `rows` valid rows.  32x32
 // result: lane -> token lane & 31; element i -> weight row 8 (i / 4) + 4 (lane /
 // 32) + i % 4.
-template <int SA, int SB>
-__device__ __forceinline__ void store_tile(const GemmArgs &p, const f32x16 (&y)[SA][SB], int64_t n0, int64_t m0,
+template <int SA, int SB, class Sub>
+__device__ __forceinline__ void store_tile(const GemmArgs &p, const Sub (&y)[SA][SB], int64_t n0, int64_t m0,
                                            int64_t rows, int ml0, int lane) {
     const int rr = lane & 31, hi = lane >> 5;
 #pragma unroll
@@ -654,11 +654,11 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     const uint32_t lds0 = lds_address(lds);
     const uint32_t wlds = lds0 + wn * 16384 + wm * 1024, xlds = lds0 + kX + wave * 1024;
     const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
-    // the lane's offsets, out of range in blocks where its piece lies past K
+    // the lane's offsets: out of range for good once its piece lies past K
     uint32_t wv = wgo, xv = xgo;
     auto aim = [&](int kb) __attribute__((always_inline)) {
-        wv = kb < kb_in ? wgo : kOobOffset;
-        xv = kb < kb_in ? xgo : kOobOffset;
+        wv = kb < kb_in ? wv : kOobOffset;
+        xv = kb < kb_in ? xv : kOobOffset;
     };
     // (st: the stage, kb & 1; wv and xv aimed at kb)
     auto fill_w = [&](const int st, const int a, int kb) __attribute__((always_inline)) {
@@ -698,16 +698,25 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     f32x16 zero16;
 #pragma unroll
     for (int i = 0; i < 16; ++i) zero16[i] = 0.f;
-    f32x16 y[SA][SB], acc[SB];
+    f32x16 acc[SB];
+    float y[SA][SB][16];   // (single registers: vectors of 16 would need room to be moved)
     float tb[SB], xsv[SB], wsv = 0.f;
 #pragma unroll
     for (int b = 0; b < SB; ++b) {
         acc[b] = zero16;
         tb[b] = 0.f;
 #pragma unroll
-        for (int a = 0; a < SA; ++a) y[a][b] = zero16;
+        for (int a = 0; a < SA; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[a][b][i] = 0.f;
     }
-    i32x4 xf[SB][4], wf[4];
+    // activation fragments: sub-row 0 of even and of odd blocks, sub-row 1
+    i32x4 xf[3][4], wf[4];
+    auto read_x = [&](i32x4 (&f)[4], const int st, const int b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            f[s] = *reinterpret_cast<const i32x4 *>(lds + xfrag[s] + (st * kStage + b * 4096));
+    };
 
     // elements [i0, i0 + n) of sub-tile (a, b)
     auto rescale = [&](const int a, const int b, const int i0, const int n) __attribute__((always_inline)) {
@@ -716,7 +725,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 #pragma unroll
         for (int i = i0; i < i0 + n; ++i) asm volatile("" ::"v"(y[a][b][i]));
     };
-    // Memory phase of cluster a of block kb, in stage st.  Fills, in this order
+    // Memory phase of cluster a of block kb, in stage st.  It reads the weight
+    // fragments of its cluster and, of the activations, sub-row 1 in a = 0 and
+    // the next block's sub-row 0 in a = 3: 8, 4, 4, 8 reads.  Fills, in this order
     // from block to block:
     //   a = 1: activation pieces 0, 1 of kb + 2    a = 2: pieces 2, 3
     //   a = 3: weight sub-rows 0, 1 of kb + 2      a = 0: sub-rows 2, 3 of kb + 1
@@ -727,11 +738,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) wf[s] = *reinterpret_cast<const i32x4 *>(lds + wfrag[s] + (st * kStage + a * 4096));
         if constexpr (a == 0) {
-#pragma unroll
-            for (int b = 0; b < SB; ++b)
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    xf[b][s] = *reinterpret_cast<const i32x4 *>(lds + xfrag[s] + (st * kStage + b * 4096));
+            read_x(xf[2], st, 1);
 #pragma unroll
             for (int b = 0; b < SB; ++b)
                 xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
@@ -748,6 +755,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
             fill_x(st, 2, kb + 2);
             fill_x(st, 3, kb + 2);
         } else {
+            read_x(xf[st ^ 1], st ^ 1, 0);
             fill_w(st, 0, kb + 2);
             fill_w(st, 1, kb + 2);
         }
@@ -755,8 +763,10 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
         rescale((a + 3) % 4, 0, 0, 16);
         if constexpr (a == 1)
             wait_lds<10>();   // weight sub-rows 2, 3 of this block are in
+        else if constexpr (a == 2)
+            wait_lds<8>();    // the activation rows of the next block
         else if constexpr (a == 3)
-            wait_lds<8>();    // the activation rows and sub-rows 0, 1 of the next block
+            wait_lds<8>();    // weight sub-rows 0, 1 of the next block
         else
             wait_lds<63>();
         __builtin_amdgcn_sched_barrier(0);
@@ -765,14 +775,14 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     // previous cluster's second sub-tile (that of the first runs in the memory
     // phase): each wave's vector work is spread over both phases, and neither
     // waits for an MFMA that has just been issued.
-    auto math = [&](auto ac) __attribute__((always_inline)) {
-        constexpr int a = decltype(ac)::value, before = (a + 3) % 4;
-        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[0][0], xf[0][1]),
+    auto math = [&](auto ac, auto sc) __attribute__((always_inline)) {
+        constexpr int a = decltype(ac)::value, before = (a + 3) % 4, x0 = decltype(sc)::value;
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[x0][0], xf[x0][1]),
                                                                  zero16, 0, 0, 0, 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
         rescale(before, 1, 0, 8);
         __builtin_amdgcn_sched_barrier(0);
-        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[0][2], xf[0][3]),
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[x0][2], xf[x0][3]),
                                                                  acc[0], 0, 0, 0, 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
         rescale(before, 1, 8, 8);
@@ -781,9 +791,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
             for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
         }
         __builtin_amdgcn_sched_barrier(0);
-        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[1][0], xf[1][1]),
+        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[2][0], xf[2][1]),
                                                                  zero16, 0, 0, 0, 0, 0, 0);
-        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[1][2], xf[1][3]),
+        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[2][2], xf[2][3]),
                                                                  acc[1], 0, 0, 0, 0, 0, 0);
 #pragma unroll
         for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(acc[b]));
@@ -792,7 +802,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
         memory(ac, sc, kb);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        math(ac);
+        math(ac, sc);
         __builtin_amdgcn_sched_barrier(0);
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -814,6 +824,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     }
     wait_lds<8>();
     lds_barrier();
+    read_x(xf[0], 0, 0);
     if (wn == 1) lds_barrier();   // group 1 runs one phase behind
     for (int kb = 0;;) {
         block(std::integral_constant<int, 0>{}, kb);
