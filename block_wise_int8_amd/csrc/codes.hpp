@@ -123,16 +123,45 @@ __device__ __forceinline__ void unpack_bf16x8(const u32x4 &v, float (&f)[8]) {
     }
 }
 
-// Store the first n of 8 bf16 values at a 2-byte aligned address: one 16-byte
-// store where the chunk is whole and aligned, else 2-byte stores.
-__device__ __forceinline__ void store_bf16x8_any(uint16_t *p, const u32x4 &v, int64_t n) {
-    if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        *reinterpret_cast<u32x4 *>(p) = v;
+// 16 bytes at any 2-byte, 8 bytes at any byte address: single instructions, the
+// hardware takes global accesses at any byte.
+struct __attribute__((packed, aligned(2))) Any16 {
+    u32x4 v;
+};
+struct __attribute__((packed, aligned(1))) Any8 {
+    uint32_t lo, hi;
+};
+
+// The first n of the 8 bf16 values at p, zeros behind them.
+__device__ __forceinline__ u32x4 load_bf16x8(const uint16_t *p, int64_t n) {
+    if (n >= 8) return reinterpret_cast<const Any16 *>(p)->v;
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) v[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+    return v;
+}
+
+// Store the first n of 8 bf16 values, of 8 codes.
+__device__ __forceinline__ void store_bf16x8(uint16_t *p, const u32x4 &v, int64_t n) {
+    if (n >= 8) {
+        reinterpret_cast<Any16 *>(p)->v = v;
         return;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (j < n) p[j] = (uint16_t)((v[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+}
+
+__device__ __forceinline__ void store_codes(void *p, uint32_t lo, uint32_t hi, int64_t n) {
+    if (n >= 8) {
+        *reinterpret_cast<Any8 *>(p) = Any8{lo, hi};
+        return;
+    }
+    uint8_t *b = static_cast<uint8_t *>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) b[j] = (uint8_t)((j < 4 ? lo : hi) >> (8 * (j & 3)));
 }
 
 }  // namespace bi8

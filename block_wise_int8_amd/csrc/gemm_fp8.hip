@@ -35,12 +35,17 @@ __device__ __forceinline__ i32x8 join16(i32x4 a, i32x4 b) {
 // Skinny path: few tokens, the weight streamed
 // ---------------------------------------------------------------------------
 //
-// Bound by HBM: N K bytes of weight against 2 M N K operations.  A workgroup
-// owns 16 weight rows and its 8 waves split K, so that at N = 4096 each CU has
-// one workgroup with its whole 64 KB share of the weight in flight.  A lane
-// loads 32 bytes of weight per K block straight into registers, every load of
-// U blocks is issued before the first MFMA, and the waves' partial sums meet in
-// LDS.
+// Bound by HBM: N K bytes of weight against 2 M N K operations.  `parts` of a
+// workgroup's 8 waves split the K of 16 weight rows; with K short enough for
+// fewer parts the other waves take further rows, so that every wave has U
+// blocks (8 KB of weight) in flight.  At K = 4096 all 8 split it, and at
+// N = 4096 each CU has one workgroup with its whole 64 KB share in flight.  A
+// lane loads 32 bytes of weight per K block straight into registers, every
+// load of U blocks is issued before the first MFMA, and the parts' sums meet
+// in LDS.
+//
+// Measured (weights from HBM): 8 x 4096 x 4096 7.2 us; grouped, 16 rows over 8
+// experts of 28672 x 4096 (940 MB) 148 us, 6.35 TB/s.
 //
 // Rows [a, b) of the activations share the weight; they are taken 16 MT at a
 // time.  Dense: [0, M), chunks over blockIdx.y.  MOE: one expert's segment, all
@@ -50,43 +55,50 @@ constexpr int kSkinnyWaves = 8;
 constexpr int kSkinnyUnroll = 4;
 
 template <int MT, bool ODD, bool MOE>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(GemmArgs p, int32_t blocks_per_wave) {
+__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(GemmArgs p, int32_t blocks_per_wave,
+                                                                                   int32_t parts) {
     constexpr int U = MT <= 3 ? kSkinnyUnroll : 2;
     constexpr int kRows = 16 * MT;
     __shared__ float red[kSkinnyWaves][MT][64][4];
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = kSkinnyWaves / parts;   // weight tiles of this workgroup
+    const int part = wave & (parts - 1);      // (parts is a power of two)
+    const int mine = wave / parts;
     const int row = lane & 15;    // weight row in the tile, and token column
     const int quad = lane >> 4;   // 32-byte quarter of a K block
-    const int64_t K = p.K, KB = p.KB;
+    const int K = (int)p.K, KB = (int)p.KB;   // (K <= 2^23: offsets inside 64 rows fit 32 bits)
 
     int64_t n0, a = 0, b = p.M;
     const int8_t *w = p.w;
     const float *ws = p.ws;
     if constexpr (MOE) {
         const uint32_t e = blockIdx.x / (uint32_t)p.tiles_n;
-        n0 = (int64_t)(blockIdx.x - e * (uint32_t)p.tiles_n) * 16;
+        n0 = (int64_t)(blockIdx.x - e * (uint32_t)p.tiles_n) * 16 * tiles;
         a = p.offsets[e];
         b = p.offsets[e + 1];
         a = a < 0 ? 0 : (a > p.M ? p.M : a);
         b = b < a ? a : (b > p.M ? p.M : b);
-        w += (int64_t)e * p.N * K;
-        ws += (int64_t)e * p.NB * KB;
+        w += (int64_t)e * p.N * p.K;
+        ws += (int64_t)e * p.NB * p.KB;
     } else {
-        n0 = (int64_t)blockIdx.x * 16;
+        n0 = (int64_t)blockIdx.x * 16 * tiles;
     }
+    const int64_t wg_n0 = n0;
+    n0 += mine * 16;
 
     // (ranges of at most 2^31 bytes: 16 MT rows of K <= 2^23)
-    const int64_t wrows = p.N - n0 < 16 ? p.N - n0 : 16;
+    const int wrows = p.N - n0 < 16 ? (p.N > n0 ? (int)(p.N - n0) : 0) : 16;   // (0: a wave without rows)
+    if (wrows == 0) n0 = wg_n0;
     uint32_t wd = 0;
     const __amdgpu_buffer_rsrc_t wr =
-        ODD ? make_rsrc_any(w + n0 * K, wrows * K, wd) : make_rsrc(w + n0 * K, clamp_bytes(wrows * K));
-    const float *ws_row = ws + (n0 / kBlock) * KB;
+        ODD ? make_rsrc_any(w + n0 * p.K, wrows * K, wd) : make_rsrc(w + n0 * p.K, (uint32_t)(wrows * K));
+    const float *ws_row = ws + (n0 / kBlock) * p.KB;
     auto load = [&](__amdgpu_buffer_rsrc_t r, uint32_t off) __attribute__((always_inline)) {
         return as_i32x4(ODD ? buf_load16_any(r, off) : buf_load16(r, off));
     };
-    const int64_t b_begin = (int64_t)wave * blocks_per_wave;
-    const int64_t b_end = b_begin + blocks_per_wave < KB ? b_begin + blocks_per_wave : KB;
+    const int b_begin = part * blocks_per_wave;
+    const int b_end = b_begin + blocks_per_wave < KB ? b_begin + blocks_per_wave : KB;
 
     // Weight loads in whole 128-byte lines: load lane l reads piece l % 8 of
     // tile row l / 8 (and of row 8 + l / 8); the MFMA wants pieces 2q, 2q + 1 of
@@ -96,25 +108,25 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
     const bool upper = row >= 8;
 
     for (int64_t m0 = a + (int64_t)blockIdx.y * kRows; m0 < b; m0 += (int64_t)gridDim.y * kRows) {
-        const int64_t mrows = b - m0 < kRows ? b - m0 : kRows;
+        const int mrows = b - m0 < kRows ? (int)(b - m0) : kRows;
         uint32_t xd = 0;
-        const __amdgpu_buffer_rsrc_t xr = ODD ? make_rsrc_any(p.xq + m0 * K, mrows * K, xd)
-                                              : make_rsrc(p.xq + m0 * K, clamp_bytes(mrows * K));
-        const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.xs + m0 * KB, clamp_bytes(mrows * KB * 4));
+        const __amdgpu_buffer_rsrc_t xr = ODD ? make_rsrc_any(p.xq + m0 * p.K, mrows * K, xd)
+                                              : make_rsrc(p.xq + m0 * p.K, (uint32_t)(mrows * K));
+        const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.xs + m0 * p.KB, (uint32_t)(mrows * KB * 4));
         f32x4 yv[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) yv[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-        for (int64_t b0 = b_begin; b0 < b_end; b0 += U) {
+        for (int b0 = b_begin; b0 < b_end; b0 += U) {
             i32x4 wa[U][2];
             i32x4 xb[U][MT][2];
             float xsv[U][MT];
             float wsv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t kb = b0 + u;
+                const int kb = b0 + u;
                 const bool ok = kb < b_end;
-                const int64_t kk = kb * kBlock + quad * 32;
+                const int kk = kb * kBlock + quad * 32;
                 const bool in0 = ok && kk < K, in1 = ok && kk + 16 < K;
                 if constexpr (ODD) {
                     // (a weight byte past K would meet a zeroed activation
@@ -122,14 +134,14 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
                     wa[u][0] = keep_bytes(load(wr, in0 ? (uint32_t)(wd + row * K + kk) : kOobOffset), K - kk);
                     wa[u][1] = keep_bytes(load(wr, in1 ? (uint32_t)(wd + row * K + kk + 16) : kOobOffset), K - kk - 16);
                 } else {
-                    const int64_t kc = kb * kBlock + lchunk * 16;
+                    const int kc = kb * kBlock + lchunk * 16;
                     const bool inl = ok && kc < K;
                     wa[u][0] = load(wr, inl ? (uint32_t)(lrow * K + kc) : kOobOffset);
                     wa[u][1] = load(wr, inl ? (uint32_t)((lrow + 8) * K + kc) : kOobOffset);
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const int64_t tok = mt * 16 + row;   // relative to m0
+                    const int tok = mt * 16 + row;   // relative to m0
                     xb[u][mt][0] = i32x4{0, 0, 0, 0};
                     xb[u][mt][1] = i32x4{0, 0, 0, 0};
                     xsv[u][mt] = 0.f;
@@ -149,7 +161,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (b0 + u >= b_end) break;   // (the scale of a block past the end is another block's)
+                const bool ok = b0 + u < b_end;
                 i32x8 wf;
                 if constexpr (ODD) {
                     wf = join16(wa[u][0], wa[u][1]);
@@ -168,7 +180,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
                 for (int mt = 0; mt < MT; ++mt) {
                     const f32x4 acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                         wf, join16(xb[u][mt][0], xb[u][mt][1]), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-                    const float t = xsv[u][mt] * wsv[u];
+                    const float t = ok ? xsv[u][mt] * wsv[u] : 0.f;   // (past the end: another block's scale)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) yv[mt][i] = fmaf(acc[i], t, yv[mt][i]);
                 }
@@ -181,13 +193,12 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
 #pragma unroll
             for (int i = 0; i < 4; ++i) red[wave][mt][lane][i] = yv[mt][i];
         __syncthreads();
-        for (int t = threadIdx.x; t < MT * 256; t += kSkinnyWaves * 64) {
-            const int mt = t >> 8, c = (t >> 4) & 15, r = t & 15;
+        for (int t = threadIdx.x; t < tiles * MT * 256; t += kSkinnyWaves * 64) {
+            const int tile = t / (MT * 256), mt = (t >> 8) % MT, c = (t >> 4) & 15, r = t & 15;
             const int src = c + 16 * (r >> 2), i = r & 3;
             float s = 0.f;
-#pragma unroll
-            for (int v = 0; v < kSkinnyWaves; ++v) s += red[v][mt][src][i];
-            const int64_t ml = mt * 16 + c, n = n0 + r;
+            for (int v = 0; v < parts; ++v) s += red[tile * parts + v][mt][src][i];
+            const int64_t ml = mt * 16 + c, n = wg_n0 + tile * 16 + r;
             if (ml < mrows && n < p.N) {
                 if (p.bias) s += bf16_bits_to_f32(p.bias[n]);
                 p.y[(m0 + ml) * p.N + n] = (uint16_t)(f32x2_to_bf16x2_bits(s, 0.0f) & 0xFFFFu);
@@ -200,13 +211,16 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
 // chunks: workgroups that share the rows of one weight tile (dense)
 template <int MT, bool ODD, bool MOE>
 hipError_t launch_skinny_mt(GemmArgs p, int64_t chunks, hipStream_t stream) {
-    p.tiles_n = (p.N + 15) / 16;
+    int32_t parts = kSkinnyWaves;
+    while (parts > 1 && p.KB <= parts / 2 * kSkinnyUnroll) parts /= 2;
+    const int64_t rows = 16 * (kSkinnyWaves / parts);
+    p.tiles_n = (p.N + rows - 1) / rows;
     const int64_t blocks = p.tiles_n * p.E;
     if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
     if (chunks > 65535) chunks = 65535;
-    const int32_t bpw = (int32_t)((p.KB + kSkinnyWaves - 1) / kSkinnyWaves);
+    const int32_t bpw = (int32_t)((p.KB + parts - 1) / parts);
     hipLaunchKernelGGL((gemm_fp8_skinny_kernel<MT, ODD, MOE>), dim3((unsigned)blocks, (unsigned)chunks),
-                       dim3(kSkinnyWaves * 64), 0, stream, p, bpw);
+                       dim3(kSkinnyWaves * 64), 0, stream, p, bpw, parts);
     return hipGetLastError();
 }
 
@@ -220,6 +234,146 @@ hipError_t launch_skinny(const GemmArgs &p, int64_t rows, hipStream_t stream) {
         case 2: return launch_skinny_mt<2, ODD, MOE>(p, chunks, stream);
         case 3: return launch_skinny_mt<3, ODD, MOE>(p, chunks, stream);
         default: return launch_skinny_mt<4, ODD, MOE>(p, chunks, stream);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Tile order
+// ---------------------------------------------------------------------------
+//
+// Dense: gemm_common.hpp's.  Grouped: the same order (an expert's m-tiles
+// advance together along n, only the tiles that exist are spread over the
+// XCDs), with the experts' segments looked up by lanes, 64 experts a step,
+// where a walk over them one by one takes longer than a tile of a few K blocks
+// (64 experts of 2048 x 1024, a row each: 89 us against FILL_IN).
+
+// One lane's expert of the 64 from e0: its segment [a, b), clamped to [0, R],
+// its m-tiles of BM rows, and the sum of the m-tiles up to and with its own.
+struct Segment {
+    int32_t a, b;
+    uint32_t tiles, upto;
+};
+template <int BM>
+__device__ __forceinline__ Segment lane_segment(const GemmArgs &p, int32_t e0) {
+    const int lane = threadIdx.x & 63;
+    const int32_t e = e0 + lane, R = (int32_t)p.M;
+    Segment s = {0, 0, 0u, 0u};
+    if (e < p.E) {
+        s.a = p.offsets[e];
+        s.b = p.offsets[e + 1];
+        s.a = s.a < 0 ? 0 : (s.a > R ? R : s.a);
+        s.b = s.b < s.a ? s.a : (s.b > R ? R : s.b);
+        s.tiles = ((uint32_t)(s.b - s.a) + BM - 1) / BM;
+    }
+    s.upto = s.tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t v = __shfl_up(s.upto, d);
+        if (lane >= d) s.upto += v;
+    }
+    return s;
+}
+
+// The m-tiles that exist.
+template <int BM>
+__device__ __forceinline__ int64_t count_tiles_m(const GemmArgs &p) {
+    int64_t n = 0;
+    for (int32_t e0 = 0; e0 < p.E; e0 += 64) n += __builtin_amdgcn_readlane((int)lane_segment<BM>(p, e0).upto, 63);
+    return n;
+}
+
+// Tile tid of the grouped order (tid below the number of tiles that exist,
+// itself below 2^31).
+template <int BN, int BM>
+__device__ __forceinline__ bool grouped_tile(const GemmArgs &p, int64_t tid, Tile &t) {
+    uint32_t rem = (uint32_t)tid;
+    const uint32_t tn = (uint32_t)p.tiles_n;
+    for (int32_t e0 = 0; e0 < p.E; e0 += 64) {
+        const Segment s = lane_segment<BM>(p, e0);
+        const uint64_t past = __ballot(s.upto * tn > rem);
+        if (past == 0) {
+            rem -= (uint32_t)__builtin_amdgcn_readlane((int)s.upto, 63) * tn;
+            continue;
+        }
+        const int l = __builtin_ctzll(past);
+        const uint32_t cnt = (uint32_t)__builtin_amdgcn_readlane((int)s.tiles, l);
+        rem -= ((uint32_t)__builtin_amdgcn_readlane((int)s.upto, l) - cnt) * tn;
+        const int64_t a = __builtin_amdgcn_readlane(s.a, l), b = __builtin_amdgcn_readlane(s.b, l);
+        const uint32_t span = (uint32_t)kGroupMMoe * tn;
+        const uint32_t group = rem / span;
+        const uint32_t first = group * (uint32_t)kGroupMMoe;
+        const uint32_t size = cnt - first < (uint32_t)kGroupMMoe ? cnt - first : (uint32_t)kGroupMMoe;
+        const uint32_t in = rem - group * span;
+        t.n0 = (int64_t)(in / size) * BN;
+        t.m0 = a + (int64_t)(first + in % size) * BM;
+        t.rows = b - t.m0 < BM ? b - t.m0 : BM;
+        t.w = p.w + (int64_t)(e0 + l) * p.N * p.K;
+        t.ws = p.ws + (int64_t)(e0 + l) * p.NB * p.KB;
+        return true;
+    }
+    return false;
+}
+
+// This workgroup's tile; false where it has none.  TAIL: the tiles of a partial
+// last round are split over K (see tail_plan).
+template <int BN, int BM, bool MOE, int64_t GM, bool TAIL = false>
+__device__ __forceinline__ bool my_tile(const GemmArgs &p, Tile &t) {
+    if constexpr (!MOE) {
+        return decode_tile<BN, BM, false, GM>(p, t);
+    } else {
+        const int64_t total = count_tiles_m<BM>(p) * p.tiles_n;
+        int64_t whole = total;   // tiles spread over the XCDs
+        if constexpr (TAIL) {
+            const TailPlan tp = tail_plan(total, p.KB);
+            if (tp.splits > 1) {
+                whole = tp.full;
+                if ((int64_t)blockIdx.x >= tp.full) {
+                    const int64_t u = (int64_t)blockIdx.x - tp.full;
+                    if (u >= tp.tail * tp.splits) return false;
+                    t.split = (int32_t)(u % tp.splits);
+                    t.nsplit = tp.splits;
+                    t.unit = u;
+                    return grouped_tile<BN, BM>(p, tp.full + u / tp.splits, t);
+                }
+            }
+        }
+        const int64_t xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+        const int64_t q = whole >> 3, r = whole & 7;
+        if (slot >= q + (xcd < r ? 1 : 0)) return false;
+        return grouped_tile<BN, BM>(p, xcd * q + (xcd < r ? xcd : r) + slot, t);
+    }
+}
+
+// The tiles that my_tile split: their units' partial sums added in split order
+// and rounded to bf16.  A fixed grid (the tail's size is only known on the
+// device) whose waves take (tile, row) pairs in turn, 4 columns a lane.
+constexpr int kTailReduceGroups = 512;
+template <int BN, int BM>
+__global__ __launch_bounds__(256) void moe_fp8_tail_reduce_kernel(GemmArgs p) {
+    const TailPlan tp = tail_plan(count_tiles_m<BM>(p) * p.tiles_n, p.KB);
+    if (tp.splits <= 1) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t pair = (int64_t)blockIdx.x * 4 + wave; pair < tp.tail * BM; pair += (int64_t)kTailReduceGroups * 4) {
+        const int64_t i = pair / BM;
+        const int r = (int)(pair - i * BM);
+        Tile t;
+        if (!grouped_tile<BN, BM>(p, tp.full + i, t) || r >= t.rows) continue;
+        const float *slots = p.partial + i * tp.splits * (BM * BN) + (int64_t)r * BN;
+        uint16_t *yrow = p.y + (t.m0 + r) * p.N;
+        const int c = 4 * lane;
+        const int64_t n = t.n0 + c;
+        if (c >= BN || n >= p.N) continue;
+        f32x4 acc = *reinterpret_cast<const f32x4 *>(slots + c);
+        for (int32_t z = 1; z < tp.splits; ++z) acc += *reinterpret_cast<const f32x4 *>(slots + (int64_t)z * (BM * BN) + c);
+        if (p.wide_store) {
+            *reinterpret_cast<uint2 *>(yrow + n) =
+                make_uint2(f32x2_to_bf16x2_bits(acc[0], acc[1]), f32x2_to_bf16x2_bits(acc[2], acc[3]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) yrow[n + e] = (uint16_t)(f32x2_to_bf16x2_bits(acc[e], 0.0f) & 0xFFFFu);
+        }
     }
 }
 
@@ -325,7 +479,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
     __shared__ float xsl[2][C::kBM * C::kSB];
 
     Tile t;
-    if (!decode_tile<C::kBN, C::kBM, MOE, GM, MOE && SPLIT>(p, t)) return;
+    if (!my_tile<C::kBN, C::kBM, MOE, GM, MOE && SPLIT>(p, t)) return;
     if (t.rows <= 0) return;
 
     const int lane = threadIdx.x & 63;
@@ -629,7 +783,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     __shared__ float xsl[2][C::kBM * C::kSB];
 
     Tile t;
-    if (!decode_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
+    if (!my_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
     if (t.rows <= 0) return;
 
     const int lane = threadIdx.x & 63;
@@ -850,6 +1004,9 @@ template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, false, false, 8>(Gemm
 template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, true, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, true, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, true, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, false, 8>(GemmArgs);
 
@@ -891,6 +1048,99 @@ hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Choice of the kernel
+// ---------------------------------------------------------------------------
+//
+// A tile takes a time per K block that hardly depends on the problem (one
+// workgroup a CU): measured at K = 4096, with few tiles on the chip and with
+// all 256 CUs taken.  The estimate of a launch is its rounds of tiles, the
+// last one's by how full it is; split over K, a unit walks its share of the
+// blocks, and the partial sums are written and read once.  The choice is the
+// smallest estimate.
+struct Tiling {
+    Fp8Path path;
+    int bn, bm;
+    double light, full;   // us a K block
+};
+constexpr Tiling kTilings[] = {
+    {Fp8Path::kTile128x64, 128, 64, 0.52, 0.57},
+    {Fp8Path::kTile128x128, 128, 128, 0.72, 0.86},
+    {Fp8Path::kTile256x128, 256, 128, 1.07, 1.38},
+    {Fp8Path::kTile256x256, 256, 256, 1.70, 2.00},
+};
+constexpr double kCUs = 256;
+constexpr int64_t kMaxPartialBytes = 64ll << 20;
+
+struct Choice {
+    Fp8Path path = Fp8Path::kSkinny;
+    int32_t splits = 1;
+    double us = 1e30;
+};
+
+double tiles_us(const Tiling &t, double tiles, int64_t blocks) {
+    const double rounds = (double)(int64_t)(tiles / kCUs), rest = tiles - rounds * kCUs;
+    return blocks * (rounds * t.full + (rest > 0 ? t.light + (t.full - t.light) * rest / kCUs : 0));
+}
+
+// partial: bytes of fp32 partial sums that may be used (0: no split)
+Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
+    Choice best;
+    // The streaming kernel moves N K (1 + M / 16) bytes: crossovers at
+    // K = 4096 (streaming / 128 x 64, us): M = 8, N = 28672 27.7 / 28.7, M = 32,
+    // N = 14336 32.3 / 22.4, M = 64, N = 4096 16.3 / 20.2.
+    if (K % 16 != 0 || (M <= 64 && N * (16 + M) <= 360000)) return best;
+    const int64_t KB = (K + kBlock - 1) / kBlock;
+    for (const Tiling &t : kTilings) {
+        const double tiles = (double)((M + t.bm - 1) / t.bm) * (double)((N + t.bn - 1) / t.bn);
+        const bool may_split = t.bn == 128;
+        for (int32_t z = 1; z <= (may_split ? 8 : 1); ++z) {
+            const int64_t per = (KB + z - 1) / z;
+            if (z > 1 && (tiles * z > kCUs || per < 4 || z * M * N * 4 > partial || (KB + per - 1) / per != z)) continue;
+            const double us = tiles_us(t, tiles * z, per) + (z > 1 ? 3 + 8e-6 * z * M * N / 4 : 0);
+            if (us < best.us) {
+                best.path = t.path;
+                best.splits = z;
+                best.us = us;
+            }
+        }
+    }
+    return best;
+}
+
+// Segments are ragged and only the device knows them: R rows spread evenly over
+// the experts, and half a tile more for each.  Every expert's weight is read,
+// at 5.5 TB/s by the tiled kernels and 6.3 by the streaming one, which takes
+// more time with more rows an expert.
+Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partial) {
+    const double experts = (double)(R < E ? R : E), mean = (double)R / experts;
+    const double bytes = experts * (double)N * (double)K;
+    Choice best;
+    best.us = 3 + bytes / 6.35e6 * (1 + (mean > 2 ? (mean - 2) / 16 : 0));
+    const int64_t KB = (K + kBlock - 1) / kBlock;
+    for (const Tiling &t : kTilings) {
+        const double m = mean <= 1 ? 1 : mean / t.bm + 0.5 < 1 ? 1 : mean / t.bm + 0.5;
+        const double tiles = experts * m * (double)((N + t.bn - 1) / t.bn);
+        double us = tiles_us(t, tiles, KB);
+        int32_t splits = 1;
+        if (t.path == Fp8Path::kTile128x128 && partial >= kTailRound * t.bn * t.bm * 4 && tiles <= kCUs / 2) {
+            const double z = (double)(int64_t)(kCUs / tiles) < KB / 4.0 ? (double)(int64_t)(kCUs / tiles) : KB / 4.0;
+            const double split_us = tiles_us(t, tiles * z, (int64_t)(KB / z) + 1) + 6;
+            if (z >= 2 && split_us < us) {
+                us = split_us;
+                splits = 2;
+            }
+        }
+        us = 3 + (us < bytes / 5.5e6 ? bytes / 5.5e6 : us);
+        if (us < best.us) {
+            best.path = t.path;
+            best.splits = splits;
+            best.us = us;
+        }
+    }
+    return best;
+}
+
 GemmArgs fp8_args(const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws, const uint16_t *bias,
                   uint16_t *y, int64_t M, int64_t N, int64_t K) {
     return make_args(reinterpret_cast<const int8_t *>(xq), xs, reinterpret_cast<const int8_t *>(w), ws, bias, y, M, N,
@@ -899,32 +1149,51 @@ GemmArgs fp8_args(const uint8_t *xq, const float *xs, const uint8_t *w, const fl
 
 }  // namespace
 
-Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K) {
-    if (K % 16 != 0 || (M <= 64 && N * (16 + M) <= 360000)) return Fp8Path::kSkinny;
-    if (((M + 255) / 256) * ((N + 255) / 256) >= 256) return Fp8Path::kTile256x256;
-    if (((M + 127) / 128) * ((N + 255) / 256) >= 256) return Fp8Path::kTile256x128;
-    return Fp8Path::kTile128x64;
-}
+Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K) { return choose_dense(M, N, K, 0).path; }
 
 Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E) {
-    const int64_t mean = (R + E - 1) / E;
-    if (mean <= 32) return Fp8Path::kSkinny;
-    const int64_t wide_tiles = (int64_t)E * ((mean + 255) / 256) * ((N + 255) / 256);
-    return wide_tiles >= 1024 ? Fp8Path::kTile256x256 : Fp8Path::kTile256x128;
+    return choose_grouped(R, N, K, E, 0).path;
 }
 
-int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0; }
+int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    const Choice c = choose_dense(M, N, K, kMaxPartialBytes);
+    return c.splits > 1 ? (int64_t)c.splits * M * N * 4 : 0;
+}
 
 hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws,
                            const uint16_t *bias, uint16_t *y, int64_t M, int64_t N, int64_t K, float *workspace,
                            int64_t workspace_bytes, hipStream_t stream) {
     if (M == 0) return hipSuccess;
-    const GemmArgs p = fp8_args(xq, xs, w, ws, bias, y, M, N, K);
+    GemmArgs p = fp8_args(xq, xs, w, ws, bias, y, M, N, K);
     if (K % 16 != 0) return launch_skinny<true, false>(p, M, stream);
-    return launch_path<false>(path == Fp8Path::kAuto ? select_gemm_fp8_path(M, N, K) : path, p, stream);
+    if (path != Fp8Path::kAuto) return launch_path<false>(path, p, stream);
+    const int64_t need = workspace ? gemm_fp8_workspace_bytes(M, N, K) : 0;
+    if (need == 0 || workspace_bytes < need) return launch_path<false>(select_gemm_fp8_path(M, N, K), p, stream);
+    const Choice c = choose_dense(M, N, K, kMaxPartialBytes);
+    p.partial = workspace;
+    p.kb_per_split = (p.KB + c.splits - 1) / c.splits;
+    p.wide_store = N % 4 == 0;   // (the workspace is 16-byte aligned)
+    const hipError_t e = c.path == Fp8Path::kTile128x64
+                             ? launch_tiled<Cfg128x64, false, true, 8>(p, stream, c.splits)
+                             : launch_tiled<Cfg128x128, false, true, 8>(p, stream, c.splits);
+    if (e != hipSuccess) return e;
+    const bool vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
+    const int64_t blocks = ((vec ? M * N / 4 : M * N) + 255) / 256;
+    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (vec)
+        hipLaunchKernelGGL(splitk_reduce_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, workspace,
+                           c.splits, M, N, bias, y);
+    else
+        hipLaunchKernelGGL(splitk_reduce_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, workspace,
+                           c.splits, M, N, bias, y);
+    return hipGetLastError();
 }
 
-int64_t moe_gemm_fp8_workspace_bytes(int64_t R, int64_t N, int64_t K, int32_t E) { return 0; }
+constexpr int64_t kGroupedPartialBytes = kTailRound * 128 * 128 * (int64_t)sizeof(float);   // a slot for each unit of a round
+
+int64_t moe_gemm_fp8_workspace_bytes(int64_t R, int64_t N, int64_t K, int32_t E) {
+    return choose_grouped(R, N, K, E, kGroupedPartialBytes).splits > 1 ? kGroupedPartialBytes : 0;
+}
 
 hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const int32_t *offsets,
                                const uint8_t *w, const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K,
@@ -933,7 +1202,15 @@ hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs,
     GemmArgs p = fp8_args(xq, xs, w, ws, nullptr, y, R, N, K);
     p.offsets = offsets;
     p.E = E;
-    return launch_path<true>(path == Fp8Path::kAuto ? select_moe_gemm_fp8_path(R, N, K, E) : path, p, stream);
+    if (path != Fp8Path::kAuto) return launch_path<true>(path, p, stream);
+    const int64_t need = workspace ? moe_gemm_fp8_workspace_bytes(R, N, K, E) : 0;
+    if (need == 0 || workspace_bytes < need) return launch_path<true>(select_moe_gemm_fp8_path(R, N, K, E), p, stream);
+    p.partial = workspace;
+    hipError_t e = launch_tiled<Cfg128x128, true, true, 8>(p, stream);
+    if (e != hipSuccess) return e;
+    p.tiles_n = (N + 127) / 128;
+    hipLaunchKernelGGL((moe_fp8_tail_reduce_kernel<128, 128>), dim3(kTailReduceGroups), dim3(256), 0, stream, p);
+    return hipGetLastError();
 }
 
 }  // namespace bi8

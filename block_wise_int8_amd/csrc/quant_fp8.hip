@@ -17,7 +17,7 @@ constexpr int kQuantWaves = 4;   // waves per workgroup
 
 // A lane's chunk `j` of row `m` covers 8 columns of group g0 + 4 j.  rows: the
 // gather form (may be null); an index outside [0, src_rows) reads zeros.
-// ODD: K % 8 != 0 or rows off the 16-byte grid (see load_bf16x8_any).
+// ODD: K % 8 != 0 or rows off the 16-byte grid (see load_bf16x8).
 template <int kChunks, bool ODD>
 __global__ __launch_bounds__(kQuantWaves * 64) void quant_act_fp8_kernel(
     const uint16_t *__restrict__ x, int64_t K, int64_t ldx, uint8_t *__restrict__ xq, float *__restrict__ xs,
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(kQuantWaves * 64) void quant_act_fp8_kernel(
         const int64_t g = g0 + 4 * j, k = g * kBlock + (lane & 15) * 8;
         v[j] = u32x4{0u, 0u, 0u, 0u};
         if (g < KB && k < K && src_ok)
-            v[j] = ODD ? load_bf16x8_any(x + src * ldx + k, K - k)
+            v[j] = ODD ? load_bf16x8(x + src * ldx + k, K - k)
                        : *reinterpret_cast<const u32x4 *>(x + src * ldx + k);
     }
 #pragma unroll
@@ -47,9 +47,9 @@ __global__ __launch_bounds__(kQuantWaves * 64) void quant_act_fp8_kernel(
         uint32_t lo, hi;
         unpack_bf16x8(v[j], f);
         E4m3Codes::encode(f, s, lo, hi);
-        int8_t *dst = reinterpret_cast<int8_t *>(xq) + m * K + k;
+        uint8_t *dst = xq + m * K + k;
         if constexpr (ODD)
-            store_codes8(dst, lo, hi, K - k);
+            store_codes(dst, lo, hi, K - k);
         else
             *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
         if ((lane & 15) == 0) xs[m * KB + g] = s;
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256) void quant_weight_fp8_kernel(const uint16_t *_
         const int64_t k = k0 + 8 * c;
         v[c] = u32x4{0u, 0u, 0u, 0u};
         if (n < N && k < K)
-            v[c] = ODD ? load_bf16x8_any(w + n * ldw + k, K - k) : *reinterpret_cast<const u32x4 *>(w + n * ldw + k);
+            v[c] = ODD ? load_bf16x8(w + n * ldw + k, K - k) : *reinterpret_cast<const u32x4 *>(w + n * ldw + k);
 #pragma unroll
         for (int j = 0; j < 4; ++j) top[j] = umax<true>(top[j], v[c][j] & 0x7FFF7FFFu);
     }
@@ -139,9 +139,9 @@ __global__ __launch_bounds__(256) void quant_weight_fp8_kernel(const uint16_t *_
         uint32_t lo, hi;
         unpack_bf16x8(v[c], f);
         E4m3Codes::encode(f, s, lo, hi);
-        int8_t *dst = reinterpret_cast<int8_t *>(wq) + n * K + k;
+        uint8_t *dst = wq + n * K + k;
         if constexpr (ODD)
-            store_codes8(dst, lo, hi, K - k);
+            store_codes(dst, lo, hi, K - k);
         else
             *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
     }
@@ -153,7 +153,7 @@ hipError_t launch_quant_act_fp8(const uint16_t *x, int64_t src_rows, int64_t ldx
                                 int64_t K, uint8_t *xq, float *xs, hipStream_t stream) {
     const int64_t KB = (K + kBlock - 1) / kBlock;
     const bool odd = K % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15u) != 0;
-    const bool two = !odd && M * KB >= 8192;   // enough groups to fill the chip with two per lane
+    const bool two = M * KB >= 8192;   // enough groups to fill the chip with two per lane
     const int64_t gpw = two ? 8 : 4;           // groups per wave
     const int64_t waves_per_row = (KB + gpw - 1) / gpw;
     const int64_t total_waves = M * waves_per_row;
@@ -161,7 +161,10 @@ hipError_t launch_quant_act_fp8(const uint16_t *x, int64_t src_rows, int64_t ldx
     if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
     const dim3 grid((unsigned)blocks), block(kQuantWaves * 64);
-    if (odd)
+    if (odd && two)
+        hipLaunchKernelGGL((quant_act_fp8_kernel<2, true>), grid, block, 0, stream, x, K, ldx, xq, xs, KB,
+                           waves_per_row, total_waves, rows, src_rows);
+    else if (odd)
         hipLaunchKernelGGL((quant_act_fp8_kernel<1, true>), grid, block, 0, stream, x, K, ldx, xq, xs, KB,
                            waves_per_row, total_waves, rows, src_rows);
     else if (two)
