@@ -245,7 +245,7 @@ hipError_t launch_skinny(const GemmArgs &p, int64_t rows, hipStream_t stream) {
 // advance together along n, only the tiles that exist are spread over the
 // XCDs), with the experts' segments looked up by lanes, 64 experts a step,
 // where a walk over them one by one takes longer than a tile of a few K blocks
-// (64 experts of 2048 x 1024, a row each: 89 us against FILL_IN).
+// (64 experts of 2048 x 1024, a row each, 128 x 64 tiles: 89 us against 24).
 
 // One lane's expert of the 64 from e0: its segment [a, b), clamped to [0, R],
 // its m-tiles of BM rows, and the sum of the m-tiles up to and with its own.
@@ -377,6 +377,41 @@ __global__ __launch_bounds__(256) void moe_fp8_tail_reduce_kernel(GemmArgs p) {
     }
 }
 
+// Buffer-to-LDS fills, 16 or 4 bytes a lane: lane i's value lands at lds + 16 i
+// (4 i).  Written out as instructions: a ring is refilled while other parts of
+// it are read, in an order that the kernels' waits count, and the compiler's own
+// tracking would drain every fill at the end of each turn of a loop.  They have
+// no result register, and the memory clobber keeps LDS reads on their side.
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)(uintptr_t)(const BI8_LDS void *)p;
+}
+// (the range check covers off + soff, and knows no wrap)
+__device__ __forceinline__ void fill16(i32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory", "m0");
+}
+__device__ __forceinline__ void fill4(i32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory", "m0");
+}
+// The words of make_rsrc's buffer resource, wave-uniform.
+__device__ __forceinline__ i32x4 rsrc_words(const void *base, uint32_t num_bytes) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(base);
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF);
+    r[2] = __builtin_amdgcn_readfirstlane((int)num_bytes);
+    r[3] = 0x00020000;
+    return r;
+}
+
+// Wait until at most N buffer-to-LDS fills are in flight (63: any number) and
+// every LDS read has returned.
+template <int N>
+__device__ __forceinline__ void wait_lds() {
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
+}
+
 // ---------------------------------------------------------------------------
 // Tiled path
 // ---------------------------------------------------------------------------
@@ -384,16 +419,18 @@ __global__ __launch_bounds__(256) void moe_fp8_tail_reduce_kernel(GemmArgs p) {
 // A workgroup of WN x WM waves computes a BN x BM tile (weight rows x
 // activation rows), each wave SA x SB sub-tiles of 32 x 32.  K advances one
 // block a step through a ring of NS stages in LDS, filled by buffer-to-LDS
-// loads NS - 1 blocks ahead: rows of 128 bytes, their 16-byte pieces
-// XOR-swizzled so that the fragment reads do not conflict.  Rows past the tile
-// and pieces past K read as zero through the buffer range check, on both
-// sides (a NaN code times zero would be NaN).
+// loads: rows of 128 bytes, their 16-byte pieces XOR-swizzled so that the
+// fragment reads do not conflict.  Rows past the tile and pieces past K read as
+// zero through the buffer range check, on both sides (a NaN code times zero
+// would be NaN).
 //
-// The block sum of sub-tile j starts from zero, and is rescaled into the
-// running sum while the matrix core works on sub-tile j + 1; the last
-// sub-tile's rescale runs under the next block's barrier and first reads.
+// These tiles serve grids that leave a workgroup alone on its CU, where a block
+// takes as long as its chain of waits.  So a step reads the fragments of block
+// kb + 1 into a second set of registers while the matrix core works on block
+// kb, whose stage is refilled at once with block kb + NS; a sub-tile's sum is
+// rescaled behind the next one's MFMAs.  One barrier a block.
 // The activation scales reach LDS eight blocks at a time; the weight scale of
-// a wave's 128-row block is a scalar load one block ahead.
+// a wave's 128-row block is a scalar load a block ahead.
 template <int WN_, int WM_, int SA_, int SB_, int NS_>
 struct Cfg {
     static constexpr int WN = WN_, WM = WM_, SA = SA_, SB = SB_, NS = NS_;
@@ -414,7 +451,7 @@ struct Cfg {
     static_assert(128 % kWaveN == 0, "a wave's weight rows lie in one scale block");
     static_assert(kScaleLoads >= 1 && kBM * kSB % (64 * kWaves) == 0, "scale split");
     static_assert(kWaves % 2 == 0, "a lane's pieces share their parity");
-    static_assert(NS >= 3 && NS <= 4 && NS - 2 < kSB, "ring depth");
+    static_assert(NS >= 3 && NS <= 4, "ring depth");
 };
 
 // Store a wave's SA x SB sub-tiles as bf16, the bias added: weight rows from n0,
@@ -455,13 +492,6 @@ __device__ __forceinline__ void store_tile(const GemmArgs &p, const Sub (&y)[SA]
     }
 }
 
-// Wait until at most N buffer-to-LDS fills are in flight (63: any number) and
-// every LDS read has returned.
-template <int N>
-__device__ __forceinline__ void wait_lds() {
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0x0 << 8) | ((N >> 4) << 14));
-}
-
 // SPLIT: a workgroup sums only a run of K blocks and stores fp32 partial sums:
 // dense, run blockIdx.y of kb_per_split blocks, in p.partial[blockIdx.y];
 // grouped, the tiles of a partial last round (see tail_plan).
@@ -469,13 +499,7 @@ template <class C, bool MOE, bool SPLIT, int64_t GM>
 __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int SA = C::SA, SB = C::SB, NS = C::NS;
-    __shared__ __attribute__((aligned(1024))) char lds0[C::kStageBytes];
-    __shared__ __attribute__((aligned(1024))) char lds1[C::kStageBytes];
-    __shared__ __attribute__((aligned(1024))) char lds2[NS > 2 ? C::kStageBytes : 1];
-    __shared__ __attribute__((aligned(1024))) char lds3[NS > 3 ? C::kStageBytes : 1];
-    auto lds = [&](const int i) __attribute__((always_inline)) -> char * {
-        return i == 0 ? lds0 : i == 1 ? lds1 : i == 2 ? lds2 : lds3;
-    };
+    __shared__ __attribute__((aligned(1024))) char lds[NS * C::kStageBytes];
     __shared__ float xsl[2][C::kBM * C::kSB];
 
     Tile t;
@@ -500,9 +524,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
 
     // (ranges of at most 2^31 bytes: 256 rows of K <= 2^23)
     const int64_t wrows = p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN;
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(t.w + t.n0 * K, clamp_bytes(wrows * K));
-    const __amdgpu_buffer_rsrc_t xr = make_rsrc(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
-    const __amdgpu_buffer_rsrc_t sr = make_rsrc(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
+    const i32x4 wr = rsrc_words(t.w + t.n0 * K, clamp_bytes(wrows * K));
+    const i32x4 xr = rsrc_words(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
+    const i32x4 sr = rsrc_words(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
 
     // Piece q (1 KB) covers tile rows [8q, 8q + 8): lane i lands at row 8q + i/8,
     // 16-byte slot i % 8, which holds K piece slot ^ swz(row), swz(r) = (r & 7) ^
@@ -510,54 +534,43 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
     // so a lane's K piece is the same in all of them.
     const int r_in = lane >> 3;
     const int chunk = 16 * ((lane & 7) ^ r_in ^ (wave & 1));
-    const uint32_t go = (uint32_t)((8 * wave + r_in) * K + kb0 * kBlock + chunk);
-    const uint32_t piece_stride = (uint32_t)(8 * C::kWaves * K);
-    uint32_t sofs[C::kScaleLoads];
-#pragma unroll
-    for (int j = 0; j < C::kScaleLoads; ++j) {
-        const int f = (wave * C::kScaleLoads + j) * 64 + lane;
-        sofs[j] = (uint32_t)(((f / C::kSB) * p.KB + kb0 + (f & (C::kSB - 1))) * 4);
-    }
-    // blocks whose piece `chunk` lies inside K: kb < kb_in
-    const int kb_in = (int)((K - chunk + kBlock - 1) / kBlock - kb0);
     const int nkb = (int)KB;
-
-    // The fills of block kb named by `mask`: bit j weight piece j, bit 8 + j
-    // activation piece j, bit 16 the batch of scales that kb opens.  Blocks at
-    // or past the run's end are not loaded, but every wave issues the same
-    // number of loads (reading zero), so that the waits can count them.
-    auto issue = [&](char *stage, int kb, unsigned mask) __attribute__((always_inline)) {
-        const uint32_t kofs = (uint32_t)kb * kBlock;
-        if ((mask & 0x10000u) && (kb & (C::kSB - 1)) == 0) {
-            // (entries past the last block are the next row's, or zero: unused)
+    uint32_t off = (uint32_t)((8 * wave + r_in) * K + kb0 * kBlock + chunk);
+    const uint32_t piece_stride = (uint32_t)(8 * C::kWaves * K);
+    // the lane's piece lies inside K and the run in blocks kb < kb_in
+    const int kb_in = min((int)((K - chunk + kBlock - 1) / kBlock - kb0), nkb);
+    const uint32_t wlds = lds_address(lds) + wave * 1024, xlds = wlds + C::kXOff;
+    const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
+    // Entry (row, block) of a batch of scales at row * kSB + block; entries past
+    // the last block are the next row's, or zero: unused.
+    auto fill = [&](const int st, int kb) __attribute__((always_inline)) {
+        if ((kb & (C::kSB - 1)) == 0) {
+            const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
+            const int f = wave * C::kScaleLoads * 64 + lane;
+            const uint32_t so = (uint32_t)(((f / C::kSB) * p.KB + kb0 + (f & (C::kSB - 1))) * 4);
 #pragma unroll
             for (int j = 0; j < C::kScaleLoads; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    sr, (BI8_LDS void *)&xsl[(kb / C::kSB) & 1][(wave * C::kScaleLoads + j) * 64], 4,
-                    sofs[j] + (uint32_t)kb * 4u, 0, 0, 0);
+                fill4(sr, dst + j * 256, so, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
         }
-        const bool in = kb < kb_in && kb < nkb;
+        off = kb < kb_in ? off : kOobOffset;   // out of range for good
 #pragma unroll
         for (int j = 0; j < C::kWLoads; ++j)
-            if (mask & (1u << j))
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (BI8_LDS void *)(stage + (wave + j * C::kWaves) * 1024),
-                                                         16, in ? go + kofs + j * piece_stride : kOobOffset, 0, 0, 0);
+            fill16(wr, wlds + st * C::kStageBytes + j * (C::kWaves * 1024), off, j * piece_stride + (uint32_t)kb * kBlock);
 #pragma unroll
         for (int j = 0; j < C::kXLoads; ++j)
-            if (mask & (0x100u << j))
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    xr, (BI8_LDS void *)(stage + C::kXOff + (wave + j * C::kWaves) * 1024), 16,
-                    in ? go + kofs + j * piece_stride : kOobOffset, 0, 0, 0);
+            fill16(xr, xlds + st * C::kStageBytes + j * (C::kWaves * 1024), off, j * piece_stride + (uint32_t)kb * kBlock);
     };
 
     const int wn = wave % C::WN, wm = wave / C::WN;
     const int rr = lane & 31, hi = lane >> 5;
     const int swz = (rr & 7) ^ ((rr >> 3) & 1);
-    int frag_off[4];
+    int wfrag[4], xfrag[4];   // fragment addresses of sub-tile 0, stage 0
 #pragma unroll
-    for (int s = 0; s < 4; ++s) frag_off[s] = 16 * ((2 * s + hi) ^ swz);
-    const int wrow0 = (wn * C::kWaveN + rr) * 128;
-    const int xrow0 = C::kXOff + (wm * C::kWaveM + rr) * 128;
+    for (int s = 0; s < 4; ++s) {
+        const int piece = 16 * ((2 * s + hi) ^ swz);
+        wfrag[s] = (wn * C::kWaveN + rr) * 128 + piece;
+        xfrag[s] = C::kXOff + (wm * C::kWaveM + rr) * 128 + piece;
+    }
     const int srow = (wm * C::kWaveM + rr) * C::kSB;
 
     int64_t nbw = (t.n0 + wn * C::kWaveN) / kBlock;
@@ -569,108 +582,106 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
     f32x16 zero16;
 #pragma unroll
     for (int i = 0; i < 16; ++i) zero16[i] = 0.f;
-    f32x16 y[SA][SB];
+    f32x16 acc[2];
+    float y[SA][SB][16];   // (single registers: vectors of 16 would need room to be moved)
 #pragma unroll
     for (int a = 0; a < SA; ++a)
 #pragma unroll
-        for (int b = 0; b < SB; ++b) y[a][b] = zero16;
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[a][b][i] = 0.f;
+    acc[0] = acc[1] = zero16;
 
-    auto rescale = [&](const f32x16 &acc, f32x16 &yv, float tb) __attribute__((always_inline)) {
+    auto rescale = [&](const int j, float tb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) yv[i] = fmaf(acc[i], tb, yv[i]);
-        // (a use here keeps the rescales from sinking past the next branch,
-        // which would keep every block sum live at once)
+        for (int i = 0; i < 16; ++i) y[j / SB][j % SB][i] = fmaf(acc[j & 1][i], tb, y[j / SB][j % SB][i]);
+        // (a use here keeps the rescales where they are)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) asm volatile("" ::"v"(yv[i]));
+        for (int i = 0; i < 16; ++i) asm volatile("" ::"v"(y[j / SB][j % SB][i]));
     };
 
-    i32x4 xf[SB][4], wf0[4];
-    float xsv[SB], wsv;
-    auto read_first = [&](const char *stage, int kb) __attribute__((always_inline)) {
+    // two sets of fragments and scales: blocks of even and of odd index
+    i32x4 wf[2][SA][4], xf[2][SB][4];
+    float xsv[2][SB], wsv[2], tlast = 0.f;
+    auto read = [&](const int st, const int set, int kb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int b = 0; b < SB; ++b)
-            xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+        for (int a = 0; a < SA; ++a)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) wf0[s] = *reinterpret_cast<const i32x4 *>(stage + wrow0 + frag_off[s]);
+            for (int s = 0; s < 4; ++s)
+                wf[set][a][s] = *reinterpret_cast<const i32x4 *>(lds + wfrag[s] + (st * C::kStageBytes + a * 4096));
 #pragma unroll
         for (int b = 0; b < SB; ++b)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                xf[b][s] = *reinterpret_cast<const i32x4 *>(stage + xrow0 + b * 32 * 128 + frag_off[s]);
-        wsv = ws_cur;
+                xf[set][b][s] = *reinterpret_cast<const i32x4 *>(lds + xfrag[s] + (st * C::kStageBytes + b * 4096));
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+            xsv[set][b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+        wsv[set] = ws_cur;
         ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
     };
-    // Block kb is in LDS once this wave's fills of it have landed and every
-    // wave is past the barrier, which also ends every read of block kb - 1.
-    // Blocks kb + 1 .. kb + NS - 2 may still be in flight, with the batch of
-    // scales that one of them opens.
-    auto arrive = [&](int kb) __attribute__((always_inline)) {
-        if constexpr (NS == 2) {
-            wait_vmcnt<0>();
-        } else {
-            if ((kb & (C::kSB - 1)) >= C::kSB - (NS - 2))
-                wait_vmcnt<(NS - 2) * C::kLoads + C::kScaleLoads>();
-            else
-                wait_vmcnt<(NS - 2) * C::kLoads>();
-        }
-        lds_barrier();
-    };
-    // spread a block's fills over its first sub-tiles
     constexpr int kSub = SA * SB;
-    constexpr int kSpread = kSub >= 8 ? 4 : kSub >= 2 ? 2 : 1;
-    auto fill_mask = [](int j) {
-        unsigned m = j == 0 ? 0x10000u : 0u;
-        for (int q = 0; q < C::kWLoads; ++q)
-            if (q % kSpread == j) m |= 1u << q;
-        for (int q = 0; q < C::kXLoads; ++q)
-            if (q % kSpread == j) m |= 0x100u << q;
-        return m;
-    };
-
-    // One K block: fills of block kb + NS - 1 into the stage of block kb - 1,
-    // the sub-tiles' MFMAs, each sub-tile's rescale behind the next one's.
-    auto compute = [&](const char *stage, char *ahead, const char *nxt, int kb) __attribute__((always_inline)) {
+    // Block kb, whose fragments are in set `set` and whose stage is st.  Before
+    // the barrier this wave's reads of the stage have returned and its fills of
+    // block kb + 1 have landed (NS - 2 blocks may still be on their way; a batch
+    // of scales among them only makes the wait stricter).
+    auto step = [&](auto stc, auto setc, int kb) __attribute__((always_inline)) {
+        constexpr int st = decltype(stc)::value, set = decltype(setc)::value;
+        wait_lds<(NS - 2) * C::kLoads>();
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        read((st + 1) % NS, set ^ 1, kb + 1);   // (past the last block: read and not used)
+        fill(st, kb + NS);
+        __builtin_amdgcn_sched_barrier(0);
         float tb[SB];
 #pragma unroll
-        for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
-        f32x16 acc[2];
+        for (int b = 0; b < SB; ++b) tb[b] = xsv[set][b] * wsv[set];
 #pragma unroll
-        for (int a = 0; a < SA; ++a) {
-            i32x4 wf[4];
+        for (int j = 0; j < kSub; ++j) {
+            const i32x4(&w)[4] = wf[set][j / SB], (&x)[4] = xf[set][j % SB];
+            // (one sub-tile: two accumulators in turn from block to block)
+            constexpr int flip = kSub == 1 ? set : 0;
+            f32x16 &c = acc[(j + flip) & 1];
+            c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(w[0], w[1]), join16(x[0], x[1]), zero16, 0, 0,
+                                                                0, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(w[2], w[3]), join16(x[2], x[3]), c, 0, 0, 0, 0,
+                                                                0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (kSub == 1) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                wf[s] = a == 0 ? wf0[s]
-                               : *reinterpret_cast<const i32x4 *>(stage + wrow0 + a * 32 * 128 + frag_off[s]);
-#pragma unroll
-            for (int b = 0; b < SB; ++b) {
-                const int j = a * SB + b;
-                acc[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    join16(wf[0], wf[1]), join16(xf[b][0], xf[b][1]), zero16, 0, 0, 0, 0, 0, 0);
-                acc[j & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    join16(wf[2], wf[3]), join16(xf[b][2], xf[b][3]), acc[j & 1], 0, 0, 0, 0, 0, 0);
-                if (j < kSpread) issue(ahead, kb + NS - 1, fill_mask(j));
-                if (j > 0) rescale(acc[(j - 1) & 1], y[(j - 1) / SB][(j - 1) % SB], tb[(j - 1) % SB]);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 16; ++i) y[0][0][i] = fmaf(acc[flip ^ 1][i], tlast, y[0][0][i]);
+            } else if (j > 0) {
+                rescale(j - 1, tb[(j - 1) % SB]);
+            } else {
+                rescale(kSub - 1, tlast);   // the previous block's last sub-tile
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        asm volatile("" ::"v"(acc[(kSub - 1) & 1]));   // the last MFMAs stay ahead of the barrier
-        if (kb + 1 < nkb) {
-            arrive(kb + 1);
-            read_first(nxt, kb + 1);
-        }
-        rescale(acc[(kSub - 1) & 1], y[SA - 1][SB - 1], tb[SB - 1]);
+        tlast = tb[SB - 1];
+        asm volatile("" : "+v"(acc[0]), "+v"(acc[1]));
     };
 
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) issue(lds(i), i, 0x1FFFFu);
-    arrive(0);
-    read_first(lds0, 0);
-    for (int kb = 0; kb < nkb;) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            compute(lds(i), lds((i + NS - 1) % NS), lds((i + 1) % NS), kb);
-            if (++kb >= nkb) break;
+    for (int i = 0; i < NS; ++i) fill(i, i);
+    wait_lds<(NS - 1) * C::kLoads>();
+    lds_barrier();
+    read(0, 0, 0);
+    constexpr int kTurn = NS % 2 ? 2 * NS : NS;   // steps until stage and set are back
+    int kb = 0;
+    auto turn = [&](auto self, auto ic) __attribute__((always_inline)) -> void {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i < kTurn) {
+            step(std::integral_constant<int, i % NS>{}, std::integral_constant<int, i % 2>{}, kb);
+            if (++kb < nkb) self(self, std::integral_constant<int, i + 1>{});
         }
+    };
+    while (kb < nkb) turn(turn, std::integral_constant<int, 0>{});
+    if constexpr (kSub == 1) {
+        const int last = (nkb - 1) & 1;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[0][0][i] = fmaf(last ? acc[1][i] : acc[0][i], tlast, y[0][0][i]);
+    } else {
+        rescale(kSub - 1, tlast);
     }
     wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
 
@@ -736,34 +747,6 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
 // kb + 2 as soon as both groups have read those of kb into registers, the
 // weight sub-rows a cluster or two after they were read, so that fills run
 // between one and two blocks ahead and no wait drains them.
-//
-// The fills are written out as instructions: a region is refilled while the
-// other half of its stage is read, in an order that the waits below count, and
-// the compiler's own tracking would drain every fill at each block.  They have
-// no result register; the memory clobber keeps LDS reads on their side.
-__device__ __forceinline__ uint32_t lds_address(const void *p) {
-    return (uint32_t)(uintptr_t)(const BI8_LDS void *)p;
-}
-// (the range check covers off + soff, and knows no wrap)
-__device__ __forceinline__ void fill16(i32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory", "m0");
-}
-__device__ __forceinline__ void fill4(i32x4 rsrc, uint32_t lds, uint32_t off, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 ::"s"(lds), "v"(off), "s"(rsrc), "s"(soff) : "memory", "m0");
-}
-// The words of make_rsrc's buffer resource, wave-uniform.
-__device__ __forceinline__ i32x4 rsrc_words(const void *base, uint32_t num_bytes) {
-    const uint64_t a = reinterpret_cast<uintptr_t>(base);
-    i32x4 r;
-    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF);
-    r[2] = __builtin_amdgcn_readfirstlane((int)num_bytes);
-    r[3] = 0x00020000;
-    return r;
-}
-
 struct PingPong {
     static constexpr int kThreads = 512;
     static constexpr int kBN = 256, kBM = 256, SA = 4, SB = 2;
@@ -1005,7 +988,7 @@ template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, true, false, 8>(GemmA
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, true, 8>(GemmArgs);
-template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, true, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, false, 8>(GemmArgs);
@@ -1064,10 +1047,10 @@ struct Tiling {
     double light, full;   // us a K block
 };
 constexpr Tiling kTilings[] = {
-    {Fp8Path::kTile128x64, 128, 64, 0.52, 0.57},
-    {Fp8Path::kTile128x128, 128, 128, 0.72, 0.86},
-    {Fp8Path::kTile256x128, 256, 128, 1.07, 1.38},
-    {Fp8Path::kTile256x256, 256, 256, 1.70, 2.00},
+    {Fp8Path::kTile128x64, 128, 64, 0.42, 0.52},
+    {Fp8Path::kTile128x128, 128, 128, 0.61, 0.75},
+    {Fp8Path::kTile256x128, 256, 128, 1.10, 1.30},
+    {Fp8Path::kTile256x256, 256, 256, 1.25, 1.90},
 };
 constexpr double kCUs = 256;
 constexpr int64_t kMaxPartialBytes = 64ll << 20;
@@ -1123,7 +1106,7 @@ Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partia
         const double tiles = experts * m * (double)((N + t.bn - 1) / t.bn);
         double us = tiles_us(t, tiles, KB);
         int32_t splits = 1;
-        if (t.path == Fp8Path::kTile128x128 && partial >= kTailRound * t.bn * t.bm * 4 && tiles <= kCUs / 2) {
+        if (t.path == Fp8Path::kTile128x64 && partial >= kTailRound * t.bn * t.bm * 4 && tiles <= kCUs / 2) {
             const double z = (double)(int64_t)(kCUs / tiles) < KB / 4.0 ? (double)(int64_t)(kCUs / tiles) : KB / 4.0;
             const double split_us = tiles_us(t, tiles * z, (int64_t)(KB / z) + 1) + 6;
             if (z >= 2 && split_us < us) {
@@ -1189,7 +1172,7 @@ hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, con
     return hipGetLastError();
 }
 
-constexpr int64_t kGroupedPartialBytes = kTailRound * 128 * 128 * (int64_t)sizeof(float);   // a slot for each unit of a round
+constexpr int64_t kGroupedPartialBytes = kTailRound * 128 * 64 * (int64_t)sizeof(float);   // a slot for each unit of a round
 
 int64_t moe_gemm_fp8_workspace_bytes(int64_t R, int64_t N, int64_t K, int32_t E) {
     return choose_grouped(R, N, K, E, kGroupedPartialBytes).splits > 1 ? kGroupedPartialBytes : 0;
@@ -1206,10 +1189,10 @@ hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs,
     const int64_t need = workspace ? moe_gemm_fp8_workspace_bytes(R, N, K, E) : 0;
     if (need == 0 || workspace_bytes < need) return launch_path<true>(select_moe_gemm_fp8_path(R, N, K, E), p, stream);
     p.partial = workspace;
-    hipError_t e = launch_tiled<Cfg128x128, true, true, 8>(p, stream);
+    hipError_t e = launch_tiled<Cfg128x64, true, true, 8>(p, stream);
     if (e != hipSuccess) return e;
     p.tiles_n = (N + 127) / 128;
-    hipLaunchKernelGGL((moe_fp8_tail_reduce_kernel<128, 128>), dim3(kTailReduceGroups), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((moe_fp8_tail_reduce_kernel<128, 64>), dim3(kTailReduceGroups), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

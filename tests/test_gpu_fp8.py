@@ -297,7 +297,7 @@ SEGMENTS = [
     ([1], 16, 16), ([1, 1, 1, 1], 100, 128), ([0, 3, 0, 5, 0], 130, 272), ([2, 0, 1, 16, 17], 515, 1040),
     ([40, 0, 0, 65, 1], 256, 384), ([0, 0, 200], 300, 144), ([130, 7, 260, 0, 33], 640, 272),
     ([300, 1, 513], 1030, 256), ([1] * 70, 64, 128), ([9] * 33, 200, 160), ([700, 0, 2], 2050, 1168),
-    ([0] * 130 + [5] + [0] * 60 + [150, 3], 130, 144), ([250, 0, 301, 250], 1031, 4112), ([513, 30], 130, 2064),
+    ([0] * 130 + [5] + [0] * 60 + [150, 3], 130, 144), ([150, 0, 201, 150], 1031, 4112), ([513, 30], 130, 2064),
 ]
 
 
@@ -324,7 +324,7 @@ def test_moe_every_variant(segments, N, K, variant):
 def test_split_of_a_partial_round():
     """A grouped problem whose tiles are split over K, an exact one: split and whole agree bit for bit."""
     rng = np.random.default_rng(75)
-    segments, N, K = [250, 0, 301, 250], 1031, 4112
+    segments, N, K = [150, 0, 201, 150], 1031, 4112
     E, R = len(segments), sum(segments)
     assert bi8.moe_gemm_fp8_workspace_size(R, N, K, E) > 0
     off = np.concatenate([[0], np.cumsum(segments)]).astype(np.int32)
