@@ -978,13 +978,240 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-typedef Cfg<4, 2, 2, 2, 3> Cfg256x128;   // weight rows x activation rows
-typedef Cfg<4, 2, 1, 2, 4> Cfg128x128;
+// The same for 256 x 128 tiles, where 256 x 256 would leave CUs without a tile or
+// pad short segments: waves of 64 weight rows x 64 activation rows, group g
+// owning activation rows 64 g, a block of two clusters, and three whole stages
+// of 48 KB.
+struct PingPong128 {
+    static constexpr int kThreads = 512;
+    static constexpr int kBN = 256, kBM = 128, SA = 2, SB = 2;
+    static constexpr int kSB = 8;
+    static constexpr int kScaleLoads = kBM * kSB / 64 / 8;
+};
+
+template <bool MOE, int64_t GM>
+__global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using C = PingPong128;
+    constexpr int SA = C::SA, SB = C::SB;
+    // a stage: weight row 64 q + 32 a + i (quarter q, sub-row a), then activation rows
+    constexpr int kStage = (C::kBN + C::kBM) * 128, kX = C::kBN * 128;
+    __shared__ __attribute__((aligned(1024))) char lds[3 * kStage];
+    __shared__ float xsl[2][C::kBM * C::kSB];
+
+    Tile t;
+    if (!my_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
+    if (t.rows <= 0) return;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = wave >> 2, quarter = wave & 3;
+    const int64_t K = p.K;
+    const int nkb = (int)p.KB;
+
+    const int64_t wrows = p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN;
+    const i32x4 wr = rsrc_words(t.w + t.n0 * K, clamp_bytes(wrows * K));
+    const i32x4 xr = rsrc_words(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
+    const i32x4 sr = rsrc_words(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
+
+    // Pieces of 1 KB as in the tiled kernel.  A wave fills, of weight sub-rows a,
+    // rows 64 (wave / 4 + 2 j) + 32 a + 8 (wave % 4) + [0, 8) for j = 0, 1, and
+    // activation rows 8 (wave + 8 j).
+    const int r_in = lane >> 3;
+    const int chunk = 16 * ((lane & 7) ^ r_in ^ (wave & 1));
+    const int wrow = 64 * group + 8 * quarter;
+    const uint32_t wgo = (uint32_t)((wrow + r_in) * K + chunk);
+    const uint32_t xgo = (uint32_t)((8 * wave + r_in) * K + chunk);
+    const uint32_t rows32 = (uint32_t)(32 * K);
+    const int kb_in = (int)((K - chunk + kBlock - 1) / kBlock);
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t wlds = lds0 + wrow * 128, xlds = lds0 + kX + wave * 1024;
+    const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
+    // the lane's offsets: out of range for good once its piece lies past K
+    uint32_t wv = wgo, xv = xgo;
+    auto aim = [&](int kb) __attribute__((always_inline)) {
+        wv = kb < kb_in ? wv : kOobOffset;
+        xv = kb < kb_in ? xv : kOobOffset;
+    };
+    // (st: the stage, kb % 3; wv and xv aimed at kb)
+    auto fill_w = [&](const int st, const int a, const int j, int kb) __attribute__((always_inline)) {
+        fill16(wr, wlds + st * kStage + (a + 4 * j) * 4096, wv, (a + 4 * j) * rows32 + (uint32_t)kb * kBlock);
+    };
+    auto fill_x = [&](const int st, const int j, int kb) __attribute__((always_inline)) {
+        fill16(xr, xlds + st * kStage + j * 8192, xv, 2 * j * rows32 + (uint32_t)kb * kBlock);
+    };
+    // Entry (row, block) of a batch at row * kSB + block; entries past the last
+    // block are the next row's, or zero: unused.
+    auto fill_scales = [&](int kb) __attribute__((always_inline)) {
+        const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
+        const int f = wave * C::kScaleLoads * 64 + lane;
+        const uint32_t off = (uint32_t)(((f / C::kSB) * p.KB + (f & (C::kSB - 1))) * 4);
+#pragma unroll
+        for (int j = 0; j < C::kScaleLoads; ++j)
+            fill4(sr, dst + j * 256, off, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
+    };
+
+    const int rr = lane & 31, hi = lane >> 5;
+    const int swz = (rr & 7) ^ ((rr >> 3) & 1);
+    int wfrag[4], xfrag[4];   // fragment addresses of sub-row 0, stage 0
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int piece = 16 * ((2 * s + hi) ^ swz);
+        wfrag[s] = (quarter * 64 + rr) * 128 + piece;
+        xfrag[s] = kX + (group * 64 + rr) * 128 + piece;
+    }
+    const int srow = (group * 64 + rr) * C::kSB;
+
+    int64_t nbw = t.n0 / kBlock + quarter / 2;
+    if (nbw > p.NB - 1) nbw = p.NB - 1;
+    const BI8_CONST float *ws_row =
+        reinterpret_cast<const BI8_CONST float *>(reinterpret_cast<uintptr_t>(t.ws + nbw * p.KB));
+    float ws_cur = ws_row[0];
+
+    f32x16 zero16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) zero16[i] = 0.f;
+    f32x16 acc[SB];
+    float y[SA][SB][16];   // (single registers: vectors of 16 would need room to be moved)
+    float tb[SB], xsv[SB], wsv = 0.f;
+#pragma unroll
+    for (int b = 0; b < SB; ++b) {
+        acc[b] = zero16;
+        tb[b] = 0.f;
+#pragma unroll
+        for (int a = 0; a < SA; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[a][b][i] = 0.f;
+    }
+    // activation fragments: sub-row 0 of even and of odd blocks, sub-row 1
+    i32x4 xf[3][4], wf[4];
+    auto read_x = [&](i32x4 (&f)[4], const int st, const int b) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            f[s] = *reinterpret_cast<const i32x4 *>(lds + xfrag[s] + (st * kStage + b * 4096));
+    };
+
+    // elements [i0, i0 + n) of sub-tile (a, b)
+    auto rescale = [&](const int a, const int b, const int i0, const int n) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = i0; i < i0 + n; ++i) y[a][b][i] = fmaf(acc[b][i], tb[b], y[a][b][i]);
+#pragma unroll
+        for (int i = i0; i < i0 + n; ++i) asm volatile("" ::"v"(y[a][b][i]));
+    };
+    // Memory phase of cluster a of block kb, in stage st, set = kb % 2.  It reads
+    // the weight fragments of its cluster and, of the activations, sub-row 1 in
+    // a = 0 and the next block's sub-row 0 in a = 1: 8 reads each.  Fills of block
+    // kb + 2, into the stage that block kb - 1 has left: the activation rows and
+    // the first piece of the weight sub-rows 0 in a = 0, the others in a = 1.
+    // The waits leave the younger fills in flight (a batch of scales among
+    // them only makes a wait stricter).
+    auto memory = [&](auto ac, auto stc, auto setc, int kb) __attribute__((always_inline)) {
+        constexpr int a = decltype(ac)::value, st = decltype(stc)::value, set = decltype(setc)::value;
+        constexpr int next = (st + 1) % 3, after = (st + 2) % 3;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) wf[s] = *reinterpret_cast<const i32x4 *>(lds + wfrag[s] + (st * kStage + a * 4096));
+        if constexpr (a == 0) {
+            read_x(xf[2], st, 1);
+#pragma unroll
+            for (int b = 0; b < SB; ++b)
+                xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+            wsv = ws_cur;
+            ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
+            if (((kb + 2) & (C::kSB - 1)) == 0) fill_scales(kb + 2);
+            aim(kb + 2);
+            fill_x(after, 0, kb + 2);
+            fill_x(after, 1, kb + 2);
+            fill_w(after, 0, 0, kb + 2);
+        } else {
+            read_x(xf[set ^ 1], next, 0);
+            fill_w(after, 0, 1, kb + 2);
+            fill_w(after, 1, 0, kb + 2);
+            fill_w(after, 1, 1, kb + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        rescale(a ^ 1, 0, 0, 16);
+        if constexpr (a == 0)
+            wait_lds<7>();   // weight sub-rows 1 of this block, the activation rows of the next
+        else
+            wait_lds<8>();   // weight sub-rows 0 of the next block
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Math phase, as in the 256 x 256 kernel.
+    auto math = [&](auto ac, auto setc) __attribute__((always_inline)) {
+        constexpr int a = decltype(ac)::value, before = a ^ 1, x0 = decltype(setc)::value;
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[x0][0], xf[x0][1]),
+                                                                 zero16, 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        rescale(before, 1, 0, 8);
+        __builtin_amdgcn_sched_barrier(0);
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[x0][2], xf[x0][3]),
+                                                                 acc[0], 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        rescale(before, 1, 8, 8);
+        if constexpr (a == 0) {
+#pragma unroll
+            for (int b = 0; b < SB; ++b) tb[b] = xsv[b] * wsv;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[0], wf[1]), join16(xf[2][0], xf[2][1]),
+                                                                 zero16, 0, 0, 0, 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join16(wf[2], wf[3]), join16(xf[2][2], xf[2][3]),
+                                                                 acc[1], 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(acc[b]));
+    };
+    auto cluster = [&](auto ac, auto stc, auto setc, int kb) __attribute__((always_inline)) {
+        memory(ac, stc, setc, kb);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        math(ac, setc);
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    fill_scales(0);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+        aim(st);
+        fill_x(st, 0, st);
+        fill_x(st, 1, st);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            fill_w(st, a, 0, st);
+            fill_w(st, a, 1, st);
+        }
+    }
+    wait_lds<8>();
+    lds_barrier();
+    read_x(xf[0], 0, 0);
+    if (group == 1) lds_barrier();   // group 1 runs one phase behind
+    int kb = 0;
+    auto turn = [&](auto self, auto ic) __attribute__((always_inline)) -> void {
+        constexpr int i = decltype(ic)::value;   // kb % 6
+        if constexpr (i < 6) {
+            cluster(std::integral_constant<int, 0>{}, std::integral_constant<int, i % 3>{},
+                    std::integral_constant<int, i % 2>{}, kb);
+            cluster(std::integral_constant<int, 1>{}, std::integral_constant<int, i % 3>{},
+                    std::integral_constant<int, i % 2>{}, kb);
+            if (++kb < nkb) self(self, std::integral_constant<int, i + 1>{});
+        }
+    };
+    while (kb < nkb) turn(turn, std::integral_constant<int, 0>{});
+    if (group == 0) lds_barrier();
+    rescale(1, 0, 0, 16);
+    rescale(1, 1, 0, 16);
+    wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
+
+    store_tile<SA, SB>(p, y, t.n0 + quarter * 64, t.m0, t.rows, group * 64, lane);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+typedef Cfg<4, 2, 1, 2, 4> Cfg128x128;   // weight rows x activation rows
 typedef Cfg<4, 2, 1, 1, 4> Cfg128x64;
 
 // (the host pass has to emit the launch stubs)
-template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, false, false, 8>(GemmArgs);
-template __global__ void gemm_fp8_tiled_kernel<Cfg256x128, true, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_pingpong128_kernel<false, 8>(GemmArgs);
+template __global__ void gemm_fp8_pingpong128_kernel<true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, true, 8>(GemmArgs);
@@ -996,14 +1223,17 @@ template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, false, 8>(GemmAr
 template __global__ void gemm_fp8_pingpong_kernel<false, 4>(GemmArgs);
 template __global__ void gemm_fp8_pingpong_kernel<true, 4>(GemmArgs);
 
-template <bool MOE, int64_t GM>
+template <class C, bool MOE>
 hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
-    p.tiles_m = (p.M + 255) / 256 + (MOE ? p.E : 0);
-    p.tiles_n = (p.N + 255) / 256;
+    p.tiles_m = (p.M + C::kBM - 1) / C::kBM + (MOE ? p.E : 0);
+    p.tiles_n = (p.N + C::kBN - 1) / C::kBN;
     const int64_t total = p.tiles_m * p.tiles_n;
     if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_fp8_pingpong_kernel<MOE, GM>), dim3((unsigned)total), dim3(PingPong::kThreads), 0, stream,
-                       p);
+    if constexpr (C::kBM == 256)
+        hipLaunchKernelGGL((gemm_fp8_pingpong_kernel<MOE, 4>), dim3((unsigned)total), dim3(C::kThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((gemm_fp8_pingpong128_kernel<MOE, 8>), dim3((unsigned)total), dim3(C::kThreads), 0, stream,
+                           p);
     return hipGetLastError();
 }
 
@@ -1025,8 +1255,8 @@ hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
         case Fp8Path::kSkinny: return launch_skinny<false, MOE>(p, MOE ? (p.M + p.E - 1) / p.E : p.M, stream);
         case Fp8Path::kTile128x64: return launch_tiled<Cfg128x64, MOE, false, 8>(p, stream);
         case Fp8Path::kTile128x128: return launch_tiled<Cfg128x128, MOE, false, 8>(p, stream);
-        case Fp8Path::kTile256x128: return launch_tiled<Cfg256x128, MOE, false, 8>(p, stream);
-        case Fp8Path::kTile256x256: return launch_pingpong<MOE, 4>(p, stream);
+        case Fp8Path::kTile256x128: return launch_pingpong<PingPong128, MOE>(p, stream);
+        case Fp8Path::kTile256x256: return launch_pingpong<PingPong, MOE>(p, stream);
         default: return hipErrorInvalidValue;
     }
 }
