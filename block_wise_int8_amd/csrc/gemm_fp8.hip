@@ -405,6 +405,19 @@ __device__ __forceinline__ i32x4 rsrc_words(const void *base, uint32_t num_bytes
     return r;
 }
 
+// 16 bytes at any byte, of which the first n are a row's (zeros behind them).
+struct __attribute__((packed, aligned(1))) AnyPiece {
+    i32x4 v;
+};
+__device__ __forceinline__ i32x4 load_piece(const int8_t *p, int64_t n) {
+    if (n >= 16) return reinterpret_cast<const AnyPiece *>(p)->v;
+    i32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) v[i / 4] |= (int32_t)((uint32_t)(uint8_t)p[i] << (8 * (i % 4)));
+    return v;
+}
+
 // Wait until at most N buffer-to-LDS fills are in flight (63: any number) and
 // every LDS read has returned.
 template <int N>
@@ -495,7 +508,10 @@ __device__ __forceinline__ void store_tile(const GemmArgs &p, const Sub (&y)[SA]
 // SPLIT: a workgroup sums only a run of K blocks and stores fp32 partial sums:
 // dense, run blockIdx.y of kb_per_split blocks, in p.partial[blockIdx.y];
 // grouped, the tiles of a partial last round (see tail_plan).
-template <class C, bool MOE, bool SPLIT, int64_t GM>
+// ODD (dense, whole): K % 16 != 0, rows start at any byte.  Pieces then pass
+// through registers, a block ahead of their stage, by loads at any byte; the
+// piece that holds the end of a row is put together from its bytes.
+template <class C, bool MOE, bool SPLIT, int64_t GM, bool ODD = false>
 __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int SA = C::SA, SB = C::SB, NS = C::NS;
@@ -543,14 +559,39 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
     const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
     // Entry (row, block) of a batch of scales at row * kSB + block; entries past
     // the last block are the next row's, or zero: unused.
-    auto fill = [&](const int st, int kb) __attribute__((always_inline)) {
-        if ((kb & (C::kSB - 1)) == 0) {
-            const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
-            const int f = wave * C::kScaleLoads * 64 + lane;
-            const uint32_t so = (uint32_t)(((f / C::kSB) * p.KB + kb0 + (f & (C::kSB - 1))) * 4);
+    auto fill_scales = [&](int kb) __attribute__((always_inline)) {
+        const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
+        const int f = wave * C::kScaleLoads * 64 + lane;
+        const uint32_t so = (uint32_t)(((f / C::kSB) * p.KB + kb0 + (f & (C::kSB - 1))) * 4);
 #pragma unroll
-            for (int j = 0; j < C::kScaleLoads; ++j)
-                fill4(sr, dst + j * 256, so, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
+        for (int j = 0; j < C::kScaleLoads; ++j)
+            fill4(sr, dst + j * 256, so, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
+    };
+    i32x4 held[ODD ? C::kLoads : 1];   // ODD: the wave's pieces of the block that is next to be stored
+    auto take = [&](int kb) __attribute__((always_inline)) {
+        const int64_t k = (int64_t)kb * kBlock + chunk;
+#pragma unroll
+        for (int j = 0; j < C::kLoads; ++j) {
+            const bool weight = j < C::kWLoads;
+            const int row = 8 * (wave + (weight ? j : j - C::kWLoads) * C::kWaves) + r_in;
+            const int8_t *src = (weight ? t.w + (t.n0 + row) * K : p.xq + (t.m0 + row) * K) + k;
+            held[j] = load_piece(src, row < (weight ? wrows : t.rows) ? K - k : 0);
+        }
+    };
+    auto keep = [&](const int st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < C::kLoads; ++j) {
+            const bool weight = j < C::kWLoads;
+            const int q = wave + (weight ? j : j - C::kWLoads) * C::kWaves;
+            *reinterpret_cast<i32x4 *>(lds + st * C::kStageBytes + (weight ? 0 : C::kXOff) + q * 1024 + lane * 16) = held[j];
+        }
+    };
+    auto fill = [&](const int st, int kb) __attribute__((always_inline)) {
+        if ((kb & (C::kSB - 1)) == 0) fill_scales(kb);
+        if constexpr (ODD) {
+            keep(st);
+            take(kb + 1);
+            return;
         }
         off = kb < kb_in ? off : kOobOffset;   // out of range for good
 #pragma unroll
@@ -627,7 +668,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
     // of scales among them only makes the wait stricter).
     auto step = [&](auto stc, auto setc, int kb) __attribute__((always_inline)) {
         constexpr int st = decltype(stc)::value, set = decltype(setc)::value;
-        wait_lds<(NS - 2) * C::kLoads>();
+        // (ODD: the block's pieces were stored a step ago or more, and the loads that
+        // a store waits for are younger than a batch of scales before them)
+        wait_lds<ODD ? 63 : (NS - 2) * C::kLoads>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
         read((st + 1) % NS, set ^ 1, kb + 1);   // (past the last block: read and not used)
@@ -661,9 +704,10 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
         asm volatile("" : "+v"(acc[0]), "+v"(acc[1]));
     };
 
+    if constexpr (ODD) take(0);
 #pragma unroll
     for (int i = 0; i < NS; ++i) fill(i, i);
-    wait_lds<(NS - 1) * C::kLoads>();
+    wait_lds<ODD ? 0 : (NS - 1) * C::kLoads>();
     lds_barrier();
     read(0, 0, 0);
     constexpr int kTurn = NS % 2 ? 2 * NS : NS;   // steps until stage and set are back
@@ -1214,6 +1258,7 @@ template __global__ void gemm_fp8_pingpong128_kernel<false, 8>(GemmArgs);
 template __global__ void gemm_fp8_pingpong128_kernel<true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
+template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8, true>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, true, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, false, true, 8>(GemmArgs);
@@ -1237,14 +1282,14 @@ hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <class C, bool MOE, bool SPLIT, int64_t GM>
+template <class C, bool MOE, bool SPLIT, int64_t GM, bool ODD = false>
 hipError_t launch_tiled(GemmArgs p, hipStream_t stream, int64_t splits = 1) {
     // grouped: at least the sum over experts of ceil(rows / BM) tiles
     p.tiles_m = (p.M + C::kBM - 1) / C::kBM + (MOE ? p.E : 0);
     p.tiles_n = (p.N + C::kBN - 1) / C::kBN;
     const int64_t total = p.tiles_m * p.tiles_n + (MOE && SPLIT ? kTailRound : 0);
     if (total > 0x7FFFFFFFll || splits < 1 || splits > 65535) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_fp8_tiled_kernel<C, MOE, SPLIT, GM>), dim3((unsigned)total, (unsigned)splits),
+    hipLaunchKernelGGL((gemm_fp8_tiled_kernel<C, MOE, SPLIT, GM, ODD>), dim3((unsigned)total, (unsigned)splits),
                        dim3(C::kThreads), 0, stream, p);
     return hipGetLastError();
 }
@@ -1279,7 +1324,7 @@ struct Tiling {
 constexpr Tiling kTilings[] = {
     {Fp8Path::kTile128x64, 128, 64, 0.42, 0.52},
     {Fp8Path::kTile128x128, 128, 128, 0.61, 0.75},
-    {Fp8Path::kTile256x128, 256, 128, 1.10, 1.30},
+    {Fp8Path::kTile256x128, 256, 128, 0.92, 1.10},
     {Fp8Path::kTile256x256, 256, 256, 1.25, 1.90},
 };
 constexpr double kCUs = 256;
@@ -1296,13 +1341,19 @@ double tiles_us(const Tiling &t, double tiles, int64_t blocks) {
     return blocks * (rounds * t.full + (rest > 0 ? t.light + (t.full - t.light) * rest / kCUs : 0));
 }
 
+// Rows at any byte have two kernels: the streaming one, its loads made of
+// dwords, in chunks of 64 tokens, and 128 x 128 tiles (streaming / tiles, us: M =
+// 100, N = 4096, K = 1001 17.6 / 24.8; 2000 x 300 x 101 10.1 / 14.6; 64 x 20000 x
+// 1001 33.8 / 25.5; 300 x 8192 x 2047 96 / 38; 4096 x 8192 x 1001 492 / 184).
+bool odd_rows_streamed(int64_t M, int64_t N) { return N * (16 + M) <= 1000000; }
+
 // partial: bytes of fp32 partial sums that may be used (0: no split)
 Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
     Choice best;
     // The streaming kernel moves N K (1 + M / 16) bytes: crossovers at
     // K = 4096 (streaming / 128 x 64, us): M = 8, N = 28672 27.7 / 28.7, M = 32,
     // N = 14336 32.3 / 22.4, M = 64, N = 4096 16.3 / 20.2.
-    if (K % 16 != 0 || (M <= 64 && N * (16 + M) <= 360000)) return best;
+    if (M <= 64 && N * (16 + M) <= 360000) return best;
     const int64_t KB = (K + kBlock - 1) / kBlock;
     for (const Tiling &t : kTilings) {
         const double tiles = (double)((M + t.bm - 1) / t.bm) * (double)((N + t.bn - 1) / t.bn);
@@ -1344,7 +1395,9 @@ Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partia
                 splits = 2;
             }
         }
-        us = 3 + (us < bytes / 5.5e6 ? bytes / 5.5e6 : us);
+        // (the weight's stream and the tiles' time overlap, the shorter one not quite)
+        const double stream = bytes / 5.5e6;
+        us = 3 + (us < stream ? stream + 0.15 * us : us + 0.15 * stream);
         if (us < best.us) {
             best.path = t.path;
             best.splits = splits;
@@ -1362,13 +1415,17 @@ GemmArgs fp8_args(const uint8_t *xq, const float *xs, const uint8_t *w, const fl
 
 }  // namespace
 
-Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K) { return choose_dense(M, N, K, 0).path; }
+Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K) {
+    if (K % 16 != 0) return odd_rows_streamed(M, N) ? Fp8Path::kSkinny : Fp8Path::kTile128x128;
+    return choose_dense(M, N, K, 0).path;
+}
 
 Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E) {
     return choose_grouped(R, N, K, E, 0).path;
 }
 
 int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (K % 16 != 0) return 0;
     const Choice c = choose_dense(M, N, K, kMaxPartialBytes);
     return c.splits > 1 ? (int64_t)c.splits * M * N * 4 : 0;
 }
@@ -1378,7 +1435,9 @@ hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, con
                            int64_t workspace_bytes, hipStream_t stream) {
     if (M == 0) return hipSuccess;
     GemmArgs p = fp8_args(xq, xs, w, ws, bias, y, M, N, K);
-    if (K % 16 != 0) return launch_skinny<true, false>(p, M, stream);
+    if (K % 16 != 0)   // rows at any byte
+        return odd_rows_streamed(M, N) ? launch_skinny<true, false>(p, M, stream)
+                                       : launch_tiled<Cfg128x128, false, false, 8, true>(p, stream);
     if (path != Fp8Path::kAuto) return launch_path<false>(path, p, stream);
     const int64_t need = workspace ? gemm_fp8_workspace_bytes(M, N, K) : 0;
     if (need == 0 || workspace_bytes < need) return launch_path<false>(select_gemm_fp8_path(M, N, K), p, stream);

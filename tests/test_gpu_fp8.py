@@ -175,7 +175,8 @@ def test_gemm(M, N, K, bias):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 5, 1), (9, 40, 7), (16, 33, 130), (20, 100, 1001), (64, 50, 255), (77, 260, 402),
-                                   (300, 300, 1027), (5, 17, 9001)])
+                                   (300, 300, 1027), (5, 17, 9001), (1, 30000, 17), (65, 129, 1), (130, 140, 15), (200, 300, 129),
+                                   (257, 131, 527), (300, 700, 1543), (140, 5000, 100), (64, 20000, 33)])
 def test_gemm_rows_at_any_byte(M, N, K):
     c = product_case((62, M, N, K), M, N, K, True)
     check_product(run_gemm(*c), *fp8.gemm_f64(*c), K)
