@@ -520,7 +520,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
 
     Tile t;
     if (!my_tile<C::kBN, C::kBM, MOE, GM, MOE && SPLIT>(p, t)) return;
-    if (t.rows <= 0) return;
+    if (t.rows <= 0 || t.n0 >= p.N) return;   // (the latter: offsets that are not in order)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -811,7 +811,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 
     Tile t;
     if (!my_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
-    if (t.rows <= 0) return;
+    if (t.rows <= 0 || t.n0 >= p.N) return;   // (the latter: offsets that are not in order)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1045,7 +1045,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
 
     Tile t;
     if (!my_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
-    if (t.rows <= 0) return;
+    if (t.rows <= 0 || t.n0 >= p.N) return;   // (the latter: offsets that are not in order)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1341,19 +1341,32 @@ double tiles_us(const Tiling &t, double tiles, int64_t blocks) {
     return blocks * (rounds * t.full + (rest > 0 ? t.light + (t.full - t.light) * rest / kCUs : 0));
 }
 
+// The launch, the tiles' time and the weight's stream, which overlap, the
+// shorter one not quite.
+double overlapped_us(double tiles, double stream) {
+    return 3 + (tiles < stream ? stream + 0.15 * tiles : tiles + 0.15 * stream);
+}
+
 // Rows at any byte have two kernels: the streaming one, its loads made of
 // dwords, in chunks of 64 tokens, and 128 x 128 tiles (streaming / tiles, us: M =
 // 100, N = 4096, K = 1001 17.6 / 24.8; 2000 x 300 x 101 10.1 / 14.6; 64 x 20000 x
 // 1001 33.8 / 25.5; 300 x 8192 x 2047 96 / 38; 4096 x 8192 x 1001 492 / 184).
 bool odd_rows_streamed(int64_t M, int64_t N) { return N * (16 + M) <= 1000000; }
 
-// partial: bytes of fp32 partial sums that may be used (0: no split)
+// partial: bytes of fp32 partial sums that may be used (0: no split).
+// The streaming kernel reads the activations again for every 16 weight rows, and
+// for more than 16 tokens a wave has half the weight in flight.  Measured
+// (streaming / 128 x 64, us, weights from HBM, K = 4096): M = 1, N = 131072
+// 102 / 117, M = 8, N = 28672 28.4 / 30.9, M = 16 33.9 / 30.8, M = 32, N = 14336
+// 32.3 / 22.4, M = 64, N = 4096 16.5 / 18.9 (13.1 split over K), M = 64, N = K =
+// 2048 15.4 / 9.8, M = 16, N = 8192, K = 28672 71 / 98 (47 split).
 Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
     Choice best;
-    // The streaming kernel moves N K (1 + M / 16) bytes: crossovers at
-    // K = 4096 (streaming / 128 x 64, us): M = 8, N = 28672 27.7 / 28.7, M = 32,
-    // N = 14336 32.3 / 22.4, M = 64, N = 4096 16.3 / 20.2.
-    if (M <= 64 && N * (16 + M) <= 360000) return best;
+    const double bytes = (double)N * (double)K;
+    if (M <= 64) {
+        best.us = 4 + bytes / 5.5e6 * (1 + (M - 1) * (M <= 16 ? 0.025 : 0.047));
+        if (best.us < 2 + 0.2 * M) best.us = 2 + 0.2 * M;
+    }
     const int64_t KB = (K + kBlock - 1) / kBlock;
     for (const Tiling &t : kTilings) {
         const double tiles = (double)((M + t.bm - 1) / t.bm) * (double)((N + t.bn - 1) / t.bn);
@@ -1361,7 +1374,8 @@ Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
         for (int32_t z = 1; z <= (may_split ? 8 : 1); ++z) {
             const int64_t per = (KB + z - 1) / z;
             if (z > 1 && (tiles * z > kCUs || per < 4 || z * M * N * 4 > partial || (KB + per - 1) / per != z)) continue;
-            const double us = tiles_us(t, tiles * z, per) + (z > 1 ? 3 + 8e-6 * z * M * N / 4 : 0);
+            const double us = overlapped_us(tiles_us(t, tiles * z, per), bytes / 4.9e6) +
+                              (z > 1 ? 4 + 8e-6 * z * M * N / 4 : 0);
             if (us < best.us) {
                 best.path = t.path;
                 best.splits = z;
@@ -1395,9 +1409,7 @@ Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partia
                 splits = 2;
             }
         }
-        // (the weight's stream and the tiles' time overlap, the shorter one not quite)
-        const double stream = bytes / 5.5e6;
-        us = 3 + (us < stream ? stream + 0.15 * us : us + 0.15 * stream);
+        us = overlapped_us(us, bytes / 5.5e6);
         if (us < best.us) {
             best.path = t.path;
             best.splits = splits;

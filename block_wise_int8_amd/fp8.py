@@ -153,12 +153,12 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, bias: torch.T
 
 
 def gemm_fp8_select(M: int, N: int, K: int) -> int:
-    """The kernel variant (``GEMM_*``) that ``gemm_fp8`` runs for this shape."""
+    """The kernel variant (``GEMM_*``) that ``gemm_fp8`` runs for this shape without a workspace."""
     return int(_bi8.load().blockint8_gemm_fp8_select(M, N, K))
 
 
 def moe_gemm_fp8_select(R: int, N: int, K: int, E: int) -> int:
-    """The kernel variant (``GEMM_*``) that ``moe_gemm_fp8`` runs for this shape."""
+    """The kernel variant (``GEMM_*``) that ``moe_gemm_fp8`` runs for this shape without a workspace."""
     return int(_bi8.load().blockint8_moe_gemm_fp8_select(R, N, K, E))
 
 

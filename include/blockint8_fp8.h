@@ -143,8 +143,9 @@ int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, i
 
 /*
  * Kernel variants, as in blockint8.h: the *_select functions tell which kernel
- * blockint8_gemm_fp8 / blockint8_moe_gemm_fp8 choose for a size, the *_variant
- * forms run a named one, with the same arguments, results and errors.  Every
+ * blockint8_gemm_fp8 / blockint8_moe_gemm_fp8 choose for a size without a
+ * workspace, the *_variant forms run a named one (which leaves the workspace
+ * alone), with the same arguments, results and errors.  Every
  * variant runs every size with K % 16 == 0, dense and grouped; with K % 16 != 0
  * only BI8_GEMM_AUTO is accepted (BI8_ERR_ALIGN otherwise).  An unknown variant
  * is BI8_ERR_SHAPE.  The ids are those of blockint8.h and one more.
