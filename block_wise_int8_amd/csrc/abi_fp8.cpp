@@ -86,6 +86,11 @@ int32_t check_gemm_sizes(const char *fn, int64_t rows, int64_t N, int64_t K, int
     return check_block(fn, block_n, block_k);
 }
 
+int32_t check_experts(const char *fn, int32_t E) {
+    if (E <= 0 || E > 65536) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 65536]", fn, E);
+    return BI8_OK;
+}
+
 int32_t check_variant(const char *fn, int32_t variant, int64_t K) {
     if (variant < BI8_GEMM_AUTO || variant > BI8_GEMM_TILE_128X128)
         return fail_status(BI8_ERR_SHAPE, "%s: unknown kernel variant %d", fn, variant);
@@ -252,7 +257,7 @@ int32_t blockint8_moe_gemm_fp8_variant(int32_t variant, const uint8_t *xq, const
                                        void *workspace, int64_t workspace_bytes, void *stream) {
     static const char fn[] = "blockint8_moe_gemm_fp8";
     BI8_TRY(check_variant(fn, variant, 16));
-    if (E <= 0 || E > 65536) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 65536]", fn, E);
+    BI8_TRY(check_experts(fn, E));
     BI8_TRY(check_gemm_sizes(fn, R, N, K, block_n, block_k));
     if (K % 16 != 0) return fail_status(BI8_ERR_ALIGN, "%s: K = %lld must be a multiple of 16", fn, (long long)K);
     BI8_TRY(check_workspace(fn, workspace, workspace_bytes));
@@ -273,6 +278,27 @@ int32_t blockint8_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t
                                void *stream) {
     return blockint8_moe_gemm_fp8_variant(BI8_GEMM_AUTO, xq, xs, expert_offsets, w, ws, y, R, N, K, E, block_n, block_k,
                                           workspace, workspace_bytes, stream);
+}
+
+int32_t blockint8_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, const int32_t *expert_offsets,
+                                          const uint8_t *w13, const float *ws13, uint8_t *aq, float *as, int64_t R,
+                                          int64_t I, int64_t K, int32_t E, int32_t block_n, int32_t block_k,
+                                          void *stream) {
+    static const char fn[] = "blockint8_moe_gemm_silu_quant_fp8";
+    BI8_TRY(check_experts(fn, E));
+    if (I <= 0 || I % 128 != 0 || I > kMaxRows / 2)
+        return fail_status(BI8_ERR_SHAPE, "%s: I = %lld must be a positive multiple of 128", fn, (long long)I);
+    BI8_TRY(check_gemm_sizes(fn, R, 2 * I, K, block_n, block_k));
+    if (K % 16 != 0) return fail_status(BI8_ERR_ALIGN, "%s: K = %lld must be a multiple of 16", fn, (long long)K);
+    if (R == 0) return done(fn);
+    if (!expert_offsets || !w13 || !ws13) return null_pointer(fn);
+    BI8_TRY(check_align(fn, "expert_offsets", expert_offsets, 4));
+    BI8_TRY(check_codes(fn, xq, xs));
+    BI8_TRY(check_codes(fn, aq, as));
+    BI8_TRY(check_align(fn, "w13", w13, 16));
+    BI8_TRY(check_align(fn, "ws13", ws13, 4));
+    return bi8::call_status(fn, bi8::launch_moe_gemm_silu_quant_fp8(xq, xs, expert_offsets, w13, ws13, aq, as, R, I, K,
+                                                                    E, static_cast<hipStream_t>(stream)));
 }
 
 int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, int32_t E) {

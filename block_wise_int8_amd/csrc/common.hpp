@@ -161,8 +161,11 @@ __device__ __forceinline__ void store_codes8(int8_t *dst, uint32_t lo, uint32_t 
 // result is still a normal bf16), so there the product is formed as
 // g * (2^64 exp(g)) * u * 2^-64 with 2^64 exp(g) = exp2(g log2(e) + 64);
 // 1 + exp(g) rounds to 1.
+__device__ __forceinline__ float silu_near(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+}
 __device__ __forceinline__ float silu_times(float g, float u) {
-    if (g >= -80.0f) return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+    if (g >= -80.0f) return silu_near(g, u);
     const float t = exp2f(fmaf(g, 1.44269504088896341f, 64.0f));
     return ((g * t) * u) * 0x1p-64f;
 }

@@ -32,7 +32,7 @@ struct GemmArgs {
     float acc_bias;           // kAccBias, kept in a scalar register (see biased_acc_to_f32)
     float *partial;           // split K: fp32 partial sums [splits, M, N] (workspace)
     int64_t kb_per_split;     // split K: K blocks per split (the last split may hold fewer)
-    int8_t *aq;               // gated MoE epilogue: int8 codes [M, I] of silu(gate) * up
+    int8_t *aq;               // gated MoE epilogue: 8-bit codes [M, I] of silu(gate) * up
     float *as;                // gated MoE epilogue: their scales [M, I / 128]
     int64_t I;                // gated MoE epilogue: intermediate size (N = 2 I)
 };

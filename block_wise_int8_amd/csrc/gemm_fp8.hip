@@ -19,6 +19,7 @@
 // bring there.
 //
 // Scales and running sums are fp32; one rounding to bf16 at the store.
+#include "codes.hpp"
 #include "gemm_common.hpp"
 
 namespace bi8 {
@@ -505,6 +506,121 @@ __device__ __forceinline__ void store_tile(const GemmArgs &p, const Sub (&y)[SA]
     }
 }
 
+// LDS accesses of the wave's lanes stay on their sides of this.
+__device__ __forceinline__ void wave_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Epilogue of the gated w13 projection: the tile's gate and up columns become the
+// 128 columns t.n0 and on of a = bf16(silu(gate) up), one quantisation group, and
+// leave as codes and scales; gate, up and a are rounded to bf16 where the two
+// launches that this replaces round them, so the results are theirs bit for bit
+// wherever the sums are.
+//
+// Columns [col0, col0 + 32 SA) of token sub-tiles 0 and 1 (tile rows from ml0) are
+// the gate values of one wave and the up values of another, together pair `pair`
+// of four.  Both leave all of theirs in LDS as bf16 (after that no register of the
+// sums is needed, where the kernel has none to spare), then the gate wave
+// finishes sub-tile 0 and the up wave sub-tile 1.  A token's columns lie in lanes
+// l and l ^ 32, and with SA = 2 in those of pair ^ 1 too.
+// buf: 32 SA KB, tops: 256 words, both free once every wave is here.
+//
+// Measured, 8 experts of 28672 x 4096 (the two launches / this one, us): 512 rows
+// 195 + 10 / 197, 8192 rows 1046 + 113 / 1024.
+template <int SA>
+__device__ __forceinline__ void gate_store(const GemmArgs &p, const Tile &t, const float (&y)[SA][2][16], char *buf,
+                                           uint32_t *tops, int pair, bool gate, int col0, int ml0, int lane) {
+    constexpr int kSub = SA * 2048;     // a sub-tile's values of one wave
+    constexpr int kPieces = SA * 2;     // 16-byte pieces of a token's 32 SA codes
+    const int rr = lane & 31, hi = lane >> 5;
+    __syncthreads();   // every wave is past its last fragment read
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int c = 0; c < 2 * SA; ++c) {
+            float v[8];
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = y[c >> 1][b][8 * (c & 1) + i];
+                asm volatile("" : "+v"(v[i]));   // (or the sums would be held as pairs all along, and spill)
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = f32x2_to_bf16x2_bits(v[2 * j], v[2 * j + 1]);
+            *reinterpret_cast<u32x4 *>(buf + (4 * pair + (gate ? 0 : 2) + b) * kSub + c * 1024 + lane * 16) = o;
+        }
+    __syncthreads();
+    const int b = gate ? 0 : 1;
+    char *gates = buf + (4 * pair + b) * kSub;
+    const char *ups = gates + 2 * kSub;
+    u32x4 gv[2 * SA], av[2 * SA];
+    float gmin = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2 * SA; ++c) {
+        gv[c] = *reinterpret_cast<const u32x4 *>(gates + c * 1024 + lane * 16);
+        av[c] = *reinterpret_cast<const u32x4 *>(ups + c * 1024 + lane * 16);
+        float f[8];
+        unpack_bf16x8(gv[c], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gmin = fminf(gmin, f[i]);
+    }
+    // (silu_times takes another form for far negative gates: in a wave that has one)
+    const bool far = __any(gmin < -80.0f);
+    u32x4 top4 = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int c = 0; c < 2 * SA; ++c) {
+        float g[8], u[8], a[8];
+        unpack_bf16x8(gv[c], g);
+        unpack_bf16x8(av[c], u);
+        if (far) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = silu_times(g[i], u[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = silu_near(g[i], u[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            av[c][j] = f32x2_to_bf16x2_bits(a[2 * j], a[2 * j + 1]);
+            top4[j] = umax<true>(top4[j], av[c][j] & 0x7FFF7FFFu);
+        }
+    }
+    uint32_t top = umax<true>(umax<true>(top4[0], top4[1]), umax<true>(top4[2], top4[3]));
+    top = umax<true>(top, (uint32_t)__shfl_xor((int)top, 32));
+    if constexpr (SA == 2) {
+        if (hi == 0) tops[(2 * pair + b) * 32 + rr] = top;
+        __syncthreads();
+        top = umax<true>(top, tops[(2 * (pair ^ 1) + b) * 32 + rr]);
+    }
+    const float sc = bf16_bits_to_f32(umax<false>(top & 0xFFFFu, top >> 16)) / E4m3Codes::kMax;
+    // codes to LDS, over the gate values, a token a row of 32 SA bytes (pieces
+    // swizzled by the token), and out in whole pieces; a wave's LDS accesses run in
+    // order
+    wave_order();
+#pragma unroll
+    for (int c = 0; c < 2 * SA; ++c) {
+        float f[8];
+        uint32_t lo, up;
+        unpack_bf16x8(av[c], f);
+        E4m3Codes::encode(f, sc, lo, up);
+        char *row = gates + rr * (kPieces * 16) + (c ^ (rr & (kPieces - 1))) * 16 + 4 * hi;
+        *reinterpret_cast<uint32_t *>(row) = lo;       // columns 16 c + 4 hi
+        *reinterpret_cast<uint32_t *>(row + 8) = up;   // columns 16 c + 8 + 4 hi
+    }
+    wave_order();
+    const int64_t ml = ml0 + 32 * b;
+    if (hi == 0 && col0 == 0 && ml + rr < t.rows) p.as[(t.m0 + ml + rr) * (p.I / kBlock) + t.n0 / kBlock] = sc;
+    constexpr int kTokens = 64 / kPieces;   // tokens that a store covers
+#pragma unroll
+    for (int j = 0; j < 32 / kTokens; ++j) {
+        const int tok = kTokens * j + lane / kPieces, c = lane & (kPieces - 1);
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(gates + tok * (kPieces * 16) + (c ^ (tok & (kPieces - 1))) * 16);
+        if (ml + tok < t.rows)
+            *reinterpret_cast<i32x4 *>(p.aq + (t.m0 + ml + tok) * p.I + t.n0 + col0 + 16 * c) = v;
+    }
+}
+
 // SPLIT: a workgroup sums only a run of K blocks and stores fp32 partial sums:
 // dense, run blockIdx.y of kb_per_split blocks, in p.partial[blockIdx.y];
 // grouped, the tiles of a partial last round (see tail_plan).
@@ -798,7 +914,10 @@ struct PingPong {
     static constexpr int kScaleLoads = kBM * kSB / 64 / 8;
 };
 
-template <bool MOE, int64_t GM>
+// SILU: the grouped w13 projection with the gating and the quantisation as its
+// epilogue (see gate_store): tile rows [0, 128) are gate rows t.n0 and on, [128,
+// 256) the up rows of the same columns.
+template <bool MOE, int64_t GM, bool SILU = false>
 __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = PingPong;
@@ -810,8 +929,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     __shared__ float xsl[2][C::kBM * C::kSB];
 
     Tile t;
-    if (!my_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
-    if (t.rows <= 0 || t.n0 >= p.N) return;   // (the latter: offsets that are not in order)
+    static_assert(!SILU || MOE, "the gated epilogue is the grouped w13 projection's");
+    if (!my_tile<SILU ? C::kBN / 2 : C::kBN, C::kBM, MOE, GM>(p, t)) return;
+    if (t.rows <= 0 || t.n0 >= (SILU ? p.I : p.N)) return;   // (the latter: offsets that are not in order)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -819,8 +939,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     const int64_t K = p.K;
     const int nkb = (int)p.KB;
 
-    const int64_t wrows = p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN;
-    const i32x4 wr = rsrc_words(t.w + t.n0 * K, clamp_bytes(wrows * K));
+    // (SILU: of the wave's own half, the one whose rows it fills)
+    const int64_t wrows = SILU ? C::kBN / 2 : (p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN);
+    const i32x4 wr = rsrc_words(t.w + (SILU ? wn * p.I + t.n0 : t.n0) * K, clamp_bytes(wrows * K));
     const i32x4 xr = rsrc_words(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
     const i32x4 sr = rsrc_words(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
 
@@ -828,7 +949,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     // rows 128 wn + 32 a + 8 wm + [0, 8), and activation rows 8 (wave + 8 j).
     const int r_in = lane >> 3;
     const int chunk = 16 * ((lane & 7) ^ r_in ^ (wave & 1));
-    const uint32_t wgo = (uint32_t)((128 * wn + 8 * wm + r_in) * K + chunk);
+    const uint32_t wgo = (uint32_t)(((SILU ? 0 : 128 * wn) + 8 * wm + r_in) * K + chunk);
     const uint32_t xgo = (uint32_t)((8 * wave + r_in) * K + chunk);
     const uint32_t wstride = (uint32_t)(32 * K), xstride = (uint32_t)(64 * K);
     const int kb_in = (int)((K - chunk + kBlock - 1) / kBlock);
@@ -870,7 +991,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     }
     const int srow = (wm * 64 + rr) * C::kSB;
 
-    int64_t nbw = t.n0 / kBlock + wn;
+    int64_t nbw = (SILU ? t.n0 + wn * p.I : t.n0 + 128 * wn) / kBlock;
     if (nbw > p.NB - 1) nbw = p.NB - 1;
     const BI8_CONST float *ws_row =
         reinterpret_cast<const BI8_CONST float *>(reinterpret_cast<uintptr_t>(t.ws + nbw * p.KB));
@@ -1018,7 +1139,10 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     rescale(3, 1, 0, 16);
     wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
 
-    store_tile<SA, SB>(p, y, t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
+    if constexpr (SILU)
+        gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), wm, wn == 0, 0, wm * 64, lane);
+    else
+        store_tile<SA, SB>(p, y, t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1033,7 +1157,7 @@ struct PingPong128 {
     static constexpr int kScaleLoads = kBM * kSB / 64 / 8;
 };
 
-template <bool MOE, int64_t GM>
+template <bool MOE, int64_t GM, bool SILU = false>
 __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using C = PingPong128;
@@ -1044,8 +1168,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     __shared__ float xsl[2][C::kBM * C::kSB];
 
     Tile t;
-    if (!my_tile<C::kBN, C::kBM, MOE, GM>(p, t)) return;
-    if (t.rows <= 0 || t.n0 >= p.N) return;   // (the latter: offsets that are not in order)
+    static_assert(!SILU || MOE, "the gated epilogue is the grouped w13 projection's");
+    if (!my_tile<SILU ? C::kBN / 2 : C::kBN, C::kBM, MOE, GM>(p, t)) return;
+    if (t.rows <= 0 || t.n0 >= (SILU ? p.I : p.N)) return;   // (the latter: offsets that are not in order)
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1053,8 +1178,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     const int64_t K = p.K;
     const int nkb = (int)p.KB;
 
-    const int64_t wrows = p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN;
+    const int64_t wrows = SILU ? C::kBN / 2 : (p.N - t.n0 < C::kBN ? p.N - t.n0 : C::kBN);
     const i32x4 wr = rsrc_words(t.w + t.n0 * K, clamp_bytes(wrows * K));
+    const i32x4 wr_up = SILU ? rsrc_words(t.w + (p.I + t.n0) * K, clamp_bytes(wrows * K)) : wr;
     const i32x4 xr = rsrc_words(p.xq + t.m0 * K, clamp_bytes(t.rows * K));
     const i32x4 sr = rsrc_words(p.xs + t.m0 * p.KB, clamp_bytes(t.rows * p.KB * 4));
 
@@ -1079,7 +1205,8 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     };
     // (st: the stage, kb % 3; wv and xv aimed at kb)
     auto fill_w = [&](const int st, const int a, const int j, int kb) __attribute__((always_inline)) {
-        fill16(wr, wlds + st * kStage + (a + 4 * j) * 4096, wv, (a + 4 * j) * rows32 + (uint32_t)kb * kBlock);
+        fill16(SILU && j ? wr_up : wr, wlds + st * kStage + (a + 4 * j) * 4096, wv,
+               (SILU ? a : a + 4 * j) * rows32 + (uint32_t)kb * kBlock);
     };
     auto fill_x = [&](const int st, const int j, int kb) __attribute__((always_inline)) {
         fill16(xr, xlds + st * kStage + j * 8192, xv, 2 * j * rows32 + (uint32_t)kb * kBlock);
@@ -1106,7 +1233,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     }
     const int srow = (group * 64 + rr) * C::kSB;
 
-    int64_t nbw = t.n0 / kBlock + quarter / 2;
+    int64_t nbw = (SILU ? t.n0 + quarter / 2 * p.I : t.n0 + 64 * quarter) / kBlock;
     if (nbw > p.NB - 1) nbw = p.NB - 1;
     const BI8_CONST float *ws_row =
         reinterpret_cast<const BI8_CONST float *>(reinterpret_cast<uintptr_t>(t.ws + nbw * p.KB));
@@ -1246,7 +1373,11 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     rescale(1, 1, 0, 16);
     wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
 
-    store_tile<SA, SB>(p, y, t.n0 + quarter * 64, t.m0, t.rows, group * 64, lane);
+    if constexpr (SILU)
+        gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), 2 * group + (quarter & 1), quarter < 2, 64 * (quarter & 1), group * 64,
+                       lane);
+    else
+        store_tile<SA, SB>(p, y, t.n0 + quarter * 64, t.m0, t.rows, group * 64, lane);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1256,6 +1387,7 @@ typedef Cfg<4, 2, 1, 1, 4> Cfg128x64;
 // (the host pass has to emit the launch stubs)
 template __global__ void gemm_fp8_pingpong128_kernel<false, 8>(GemmArgs);
 template __global__ void gemm_fp8_pingpong128_kernel<true, 8>(GemmArgs);
+template __global__ void gemm_fp8_pingpong128_kernel<true, 8, true>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, true, false, 8>(GemmArgs);
 template __global__ void gemm_fp8_tiled_kernel<Cfg128x128, false, false, 8, true>(GemmArgs);
@@ -1267,17 +1399,19 @@ template __global__ void gemm_fp8_tiled_kernel<Cfg128x64, true, false, 8>(GemmAr
 
 template __global__ void gemm_fp8_pingpong_kernel<false, 4>(GemmArgs);
 template __global__ void gemm_fp8_pingpong_kernel<true, 4>(GemmArgs);
+template __global__ void gemm_fp8_pingpong_kernel<true, 4, true>(GemmArgs);
 
-template <class C, bool MOE>
+template <class C, bool MOE, bool SILU = false>
 hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
     p.tiles_m = (p.M + C::kBM - 1) / C::kBM + (MOE ? p.E : 0);
-    p.tiles_n = (p.N + C::kBN - 1) / C::kBN;
+    p.tiles_n = (p.N + C::kBN - 1) / C::kBN;   // (SILU: I / 128)
     const int64_t total = p.tiles_m * p.tiles_n;
     if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
     if constexpr (C::kBM == 256)
-        hipLaunchKernelGGL((gemm_fp8_pingpong_kernel<MOE, 4>), dim3((unsigned)total), dim3(C::kThreads), 0, stream, p);
+        hipLaunchKernelGGL((gemm_fp8_pingpong_kernel<MOE, 4, SILU>), dim3((unsigned)total), dim3(C::kThreads), 0, stream,
+                           p);
     else
-        hipLaunchKernelGGL((gemm_fp8_pingpong128_kernel<MOE, 8>), dim3((unsigned)total), dim3(C::kThreads), 0, stream,
+        hipLaunchKernelGGL((gemm_fp8_pingpong128_kernel<MOE, 8, SILU>), dim3((unsigned)total), dim3(C::kThreads), 0, stream,
                            p);
     return hipGetLastError();
 }
@@ -1390,26 +1524,36 @@ Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
 // the experts, and half a tile more for each.  Every expert's weight is read,
 // at 5.5 TB/s by the tiled kernels and 6.3 by the streaming one, which takes
 // more time with more rows an expert.
-Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partial) {
-    const double experts = (double)(R < E ? R : E), mean = (double)R / experts;
-    const double bytes = experts * (double)N * (double)K;
-    Choice best;
-    best.us = 3 + bytes / 6.35e6 * (1 + (mean > 2 ? (mean - 2) / 16 : 0));
-    const int64_t KB = (K + kBlock - 1) / kBlock;
-    for (const Tiling &t : kTilings) {
+struct Grouped {
+    double experts, mean, bytes;   // experts with rows, rows of each, bytes of their weights
+    int64_t N, KB;
+    Grouped(int64_t R, int64_t N_, int64_t K, int32_t E)
+        : experts((double)(R < E ? R : E)), mean((double)R / experts), bytes(experts * (double)N_ * (double)K), N(N_),
+          KB((K + kBlock - 1) / kBlock) {}
+    double tiles(const Tiling &t) const {
         const double m = mean <= 1 ? 1 : mean / t.bm + 0.5 < 1 ? 1 : mean / t.bm + 0.5;
-        const double tiles = experts * m * (double)((N + t.bn - 1) / t.bn);
-        double us = tiles_us(t, tiles, KB);
+        return experts * m * (double)((N + t.bn - 1) / t.bn);
+    }
+    double us(double tiles) const { return overlapped_us(tiles, bytes / 5.5e6); }
+};
+
+Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partial) {
+    const Grouped g(R, N, K, E);
+    Choice best;
+    best.us = 3 + g.bytes / 6.35e6 * (1 + (g.mean > 2 ? (g.mean - 2) / 16 : 0));
+    for (const Tiling &t : kTilings) {
+        const double tiles = g.tiles(t);
+        double us = tiles_us(t, tiles, g.KB);
         int32_t splits = 1;
         if (t.path == Fp8Path::kTile128x64 && partial >= kTailRound * t.bn * t.bm * 4 && tiles <= kCUs / 2) {
-            const double z = (double)(int64_t)(kCUs / tiles) < KB / 4.0 ? (double)(int64_t)(kCUs / tiles) : KB / 4.0;
-            const double split_us = tiles_us(t, tiles * z, (int64_t)(KB / z) + 1) + 6;
+            const double most = (double)(int64_t)(kCUs / tiles), z = most < g.KB / 4.0 ? most : g.KB / 4.0;
+            const double split_us = tiles_us(t, tiles * z, (int64_t)(g.KB / z) + 1) + 6;
             if (z >= 2 && split_us < us) {
                 us = split_us;
                 splits = 2;
             }
         }
-        us = overlapped_us(us, bytes / 5.5e6);
+        us = g.us(us);
         if (us < best.us) {
             best.path = t.path;
             best.splits = splits;
@@ -1495,6 +1639,24 @@ hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs,
     p.tiles_n = (N + 127) / 128;
     hipLaunchKernelGGL((moe_fp8_tail_reduce_kernel<128, 64>), dim3(kTailReduceGroups), dim3(256), 0, stream, p);
     return hipGetLastError();
+}
+
+hipError_t launch_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, const int32_t *offsets,
+                                          const uint8_t *w13, const float *ws13, uint8_t *aq, float *as, int64_t R,
+                                          int64_t I, int64_t K, int32_t E, hipStream_t stream) {
+    if (R == 0) return hipSuccess;
+    if (I % kBlock != 0) return hipErrorInvalidValue;
+    GemmArgs p = fp8_args(xq, xs, w13, ws13, nullptr, nullptr, R, 2 * I, K);
+    p.offsets = offsets;
+    p.E = E;
+    p.aq = reinterpret_cast<int8_t *>(aq);
+    p.as = as;
+    p.I = I;
+    const Grouped g(R, 2 * I, K, E);
+    const Tiling &small = kTilings[2], &large = kTilings[3];
+    return g.us(tiles_us(small, g.tiles(small), g.KB)) <= g.us(tiles_us(large, g.tiles(large), g.KB))
+               ? launch_pingpong<PingPong128, true, true>(p, stream)
+               : launch_pingpong<PingPong, true, true>(p, stream);
 }
 
 }  // namespace bi8

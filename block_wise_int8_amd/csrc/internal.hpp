@@ -91,6 +91,9 @@ hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, con
                            const uint16_t *bias, uint16_t *y, int64_t M, int64_t N, int64_t K, float *workspace,
                            int64_t workspace_bytes, hipStream_t stream);
 int64_t moe_gemm_fp8_workspace_bytes(int64_t R, int64_t N, int64_t K, int32_t E);
+hipError_t launch_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, const int32_t *offsets,
+                                          const uint8_t *w13, const float *ws13, uint8_t *aq, float *as, int64_t R,
+                                          int64_t I, int64_t K, int32_t E, hipStream_t stream);
 hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const int32_t *offsets,
                                const uint8_t *w, const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K,
                                int32_t E, float *workspace, int64_t workspace_bytes, hipStream_t stream);

@@ -12,7 +12,8 @@ import block_wise_int8_amd as _bi8
 from . import _call as c
 
 __all__ = ["quant_act_fp8", "quant_act_gather_fp8", "silu_mul_quant_fp8", "quant_weight_fp8", "gemm_fp8",
-           "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_fp8_workspace_size", "gemm_fp8_select",
+           "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_silu_quant_fp8",
+           "moe_gemm_fp8_workspace_size", "gemm_fp8_select",
            "moe_gemm_fp8_select", "moe_layer_fp8", "GEMM_TILE_128X128"]
 
 FP8 = torch.float8_e4m3fn
@@ -29,6 +30,7 @@ def declare(lib) -> None:
     c.declare(lib, "blockint8_gemm_fp8_workspace_size", [i64, i64, i64], i64)
     c.declare(lib, "blockint8_linear_fp8", [vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, i64, vp])
     c.declare(lib, "blockint8_moe_gemm_fp8", [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, vp])
+    c.declare(lib, "blockint8_moe_gemm_silu_quant_fp8", [vp] * 7 + [i64, i64, i64, i32, i32, i32, vp])
     c.declare(lib, "blockint8_gemm_fp8_variant", [i32] + lib.blockint8_gemm_fp8.argtypes)
     c.declare(lib, "blockint8_moe_gemm_fp8_variant", [i32] + lib.blockint8_moe_gemm_fp8.argtypes)
     c.declare(lib, "blockint8_gemm_fp8_select", [i64, i64, i64])
@@ -192,21 +194,55 @@ def moe_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: torch.Tenso
     return y
 
 
+def moe_gemm_silu_quant_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: torch.Tensor, w13: torch.Tensor,
+                            ws13: torch.Tensor, aq: torch.Tensor | None = None, as_: torch.Tensor | None = None):
+    """The w13 grouped GEMM with the SiLU gating and requantisation as its
+    epilogue: (aq float8_e4m3fn [R, I], as float32 [R, I/128]), what
+    silu_mul_quant_fp8(moe_gemm_fp8(xq, xs, expert_offsets, w13, ws13)) gives
+    up to the order of the products' sums.  w13 is float8_e4m3fn [E, 2I, K]
+    (gate rows, then up rows); I % 128 == 0."""
+    dev = c.device_of(xq, "xq")
+    c.dense(xq, "xq", dev, FP8, (None, None))
+    R, K = xq.shape
+    c.dense(w13, "w13", dev, FP8, (None, None, K))
+    E, N, _ = w13.shape
+    if N % 2:
+        raise ValueError("w13 must have an even number of rows (gate, then up)")
+    I = N // 2
+    c.dense(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
+    c.dense(xs, "xs", dev, torch.float32, (R, _blocks(K)))
+    c.dense(ws13, "ws13", dev, torch.float32, (E, _blocks(N), _blocks(K)))
+    aq = c.output(aq, "aq", dev, FP8, (R, I))
+    as_ = c.output(as_, "as_", dev, torch.float32, (R, _blocks(I)))
+    _bi8._check(c.call(_bi8.load().blockint8_moe_gemm_silu_quant_fp8, dev, xq.data_ptr(), xs.data_ptr(),
+                       expert_offsets.data_ptr(), w13.data_ptr(), ws13.data_ptr(), aq.data_ptr(), as_.data_ptr(), R, I,
+                       K, E, 128, 128))
+    return aq, as_
+
+
 def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor, w2: torch.Tensor,
                   ws2: torch.Tensor, k: int, renormalize: bool = False) -> torch.Tensor:
     """The e4m3 FusedMoE layer on the GPU: route, gather + quantise, w13 grouped
-    GEMM, SiLU gating + quantise, w2 grouped GEMM, weighted combine.  x bf16
-    [T, H]; logits fp32 [T, E]; w13 float8_e4m3fn [E, 2I, H]; w2 float8_e4m3fn
-    [E, H, I].  Returns bf16 [T, H]."""
+    GEMM, SiLU gating + quantise, w2 grouped GEMM, weighted combine.  Where the
+    w13 GEMM runs 256-row weight tiles and I % 128 == 0, it and the gating are
+    one launch (moe_gemm_silu_quant_fp8).  x bf16 [T, H]; logits fp32 [T, E];
+    w13 float8_e4m3fn [E, 2I, H]; w2 float8_e4m3fn [E, H, I].  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
     with torch.cuda.device(dev):
         _, weights, sorted_token, offsets, row_of = _bi8.moe_route(logits, k, renormalize)
         xq, xs = quant_act_gather_fp8(x, sorted_token)
         R, H = xq.shape
         E, N = w13.shape[:2]
-        nbytes = max(moe_gemm_fp8_workspace_size(R, N, H, E),
-                     moe_gemm_fp8_workspace_size(R, w2.shape[1], w2.shape[2], E))
-        wsp = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        aq, as_ = silu_mul_quant_fp8(moe_gemm_fp8(xq, xs, offsets, w13, ws13, workspace=wsp))
+        if N % 256 == 0 and moe_gemm_fp8_select(R, N, H, E) in (_bi8.GEMM_TILE_256X128, _bi8.GEMM_TILE_256X256):
+            aq, as_ = moe_gemm_silu_quant_fp8(xq, xs, offsets, w13, ws13)
+        else:
+            wsp = _layer_workspace(R, N, H, E, dev)
+            aq, as_ = silu_mul_quant_fp8(moe_gemm_fp8(xq, xs, offsets, w13, ws13, workspace=wsp))
+        wsp = _layer_workspace(R, w2.shape[1], aq.shape[1], E, dev)
         y2 = moe_gemm_fp8(aq, as_, offsets, w2, ws2, workspace=wsp)
         return _bi8.moe_combine(y2, row_of, weights)
+
+
+def _layer_workspace(R: int, N: int, K: int, E: int, dev: int):
+    nbytes = moe_gemm_fp8_workspace_size(R, N, K, E)
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None

@@ -142,6 +142,26 @@ int32_t blockint8_moe_gemm_fp8(const uint8_t *xq, const float *xs, const int32_t
 int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, int32_t E);
 
 /*
+ * The w13 grouped GEMM with the gating and its quantisation as the epilogue, as
+ * blockint8_moe_gemm_silu_quant: one launch computes what
+ * blockint8_moe_gemm_fp8 (into h, N = 2 I) followed by
+ * blockint8_silu_mul_quant_fp8 computes, without writing h.  It runs the
+ * 256 x 128 or the 256 x 256 kernel; with the same variant of the grouped GEMM
+ * the two launches give the same bits, with another the products may differ in
+ * the order of their sums.
+ *
+ *   w13   e4m3 [E, 2 I, K]: rows [0, I) gate, rows [I, 2 I) up
+ *   ws13  fp32 [E, 2 I / 128, ceil(K / 128)]
+ *   aq    e4m3 [R, I]   as  fp32 [R, I / 128]   (outputs)
+ *
+ * Errors: as blockint8_moe_gemm_silu_quant.
+ */
+int32_t blockint8_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, const int32_t *expert_offsets,
+                                          const uint8_t *w13, const float *ws13, uint8_t *aq, float *as, int64_t R,
+                                          int64_t I, int64_t K, int32_t E, int32_t block_n, int32_t block_k,
+                                          void *stream);
+
+/*
  * Kernel variants, as in blockint8.h: the *_select functions tell which kernel
  * blockint8_gemm_fp8 / blockint8_moe_gemm_fp8 choose for a size without a
  * workspace, the *_variant forms run a named one (which leaves the workspace

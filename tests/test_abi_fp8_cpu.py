@@ -25,6 +25,8 @@ CALLS = {
                        wsp=None, nbytes=0),
     "moe_gemm_fp8": dict(xq=P, xs=P, off=P, w=P, ws=P, y=P, R=4, N=256, K=256, E=2, bn=128, bk=128, wsp=None,
                          nbytes=0),
+    "moe_gemm_silu_quant_fp8": dict(xq=P, xs=P, off=P, w13=P, ws13=P, aq=P, as_=P, R=4, I=256, K=256, E=2, bn=128,
+                                    bk=128),
     "rmsnorm_quant": dict(x=P, ldx=256, residual=P, ldr=256, weight=P, eps=1e-6, M=4, H=256, bk=128, h=P, ldh=256,
                           y=None, xq=P, xs=P),
 }
@@ -70,6 +72,13 @@ BAD = {
     "moe_gemm_fp8": [b for b in PRODUCT_BAD if "ldx" not in b[0]] + [
         (dict(off=None), NULL), (dict(off=P + 2), ALIGN), (dict(E=0), SHAPE), (dict(E=65537), SHAPE),
         (dict(R=-1), SHAPE), (dict(K=100), ALIGN)],
+    "moe_gemm_silu_quant_fp8": [
+        (dict(xq=None), NULL), (dict(xs=None), NULL), (dict(off=None), NULL), (dict(w13=None), NULL),
+        (dict(ws13=None), NULL), (dict(aq=None), NULL), (dict(as_=None), NULL), (dict(R=-1), SHAPE),
+        (dict(R=1 << 31), SHAPE), (dict(I=0), SHAPE), (dict(I=200), SHAPE), (dict(I=1 << 30), SHAPE),
+        (dict(K=0), SHAPE), (dict(K=100), ALIGN), (dict(E=0), SHAPE), (dict(E=65537), SHAPE), (dict(bn=64), BLOCK),
+        (dict(bk=64), BLOCK), (dict(off=P + 2), ALIGN), (dict(xq=P + 8), ALIGN), (dict(xs=P + 2), ALIGN),
+        (dict(w13=P + 8), ALIGN), (dict(ws13=P + 2), ALIGN), (dict(aq=P + 8), ALIGN), (dict(as_=P + 2), ALIGN)],
     "rmsnorm_quant": NORM_BAD, "rmsnorm_quant_fp8": NORM_BAD,
 }
 
@@ -130,6 +139,7 @@ def test_binding_has_no_cpu_path():
     for fn in (lambda: bi8.quant_act_fp8(x), lambda: bi8.quant_act_gather_fp8(x, off),
                lambda: bi8.silu_mul_quant_fp8(x), lambda: bi8.quant_weight_fp8(x), lambda: bi8.gemm_fp8(xq, s, w, ws),
                lambda: bi8.linear_fp8(x, w, ws), lambda: bi8.moe_gemm_fp8(xq, s, off, w[None], ws[None]),
+               lambda: bi8.moe_gemm_silu_quant_fp8(xq, s, off, w[None], ws[None]),
                lambda: bi8.moe_layer_fp8(x, s, w[None], ws[None], w[None], ws[None], 1),
                lambda: bi8.rmsnorm_quant(x, x[0])):
         with pytest.raises(ValueError, match="HIP device"):

@@ -354,6 +354,58 @@ def test_moe_gemm_rows_past_the_last_segment_stay():
         check_product(y[:n], *(r[:n] for r in ref), K)
 
 
+def gated(xq, xs, off, w13, s13, **kw):
+    return bi8.moe_gemm_silu_quant_fp8(codes_dev(xq), to_dev(xs), to_dev(off), codes_dev(w13), to_dev(s13), **kw)
+
+
+@pytest.mark.parametrize("segments,I,K", [([1], 128, 16), ([0, 3, 0, 5, 0], 128, 272), ([130, 7, 260, 0, 33], 384, 528),
+                                          ([64, 65, 63], 256, 1040), ([3800], 2048, 144), ([300] * 13 + [0, 1], 1024, 400),
+                                          ([1] * 70, 128, 128)])
+def test_gated_w13_is_the_two_calls(segments, I, K):
+    """Bit for bit with the same tiles (a block's products are added in the same order by both pairs of
+    kernels); the sizes reach the 256 x 128 and the 256 x 256 kernel."""
+    xq, xs, off, w13, s13 = c = grouped_case((76, I, K), segments, 2 * I, K)
+    R = sum(segments)
+    s13[:, : I // 128] *= 4.0   # gates far enough out to reach both ends of the sigmoid
+    h = [run_grouped(*c, variant=v) for v in (bi8.GEMM_TILE_256X128, bi8.GEMM_TILE_256X256)]
+    assert torch.equal(h[0].view(torch.int16), h[1].view(torch.int16))
+    want_q, want_s = bi8.silu_mul_quant_fp8(h[0])
+    aq, as_ = gated(*c)
+    assert torch.equal(as_, want_s)
+    assert torch.equal(aq.view(torch.uint8), want_q.view(torch.uint8))
+    # outputs of the caller's, rows behind the last segment left alone
+    if R > 9:
+        off = off.copy()
+        off[off > R - 9] = R - 9
+        aq2, as2 = torch.full_like(aq.view(torch.uint8), 0x35), torch.full_like(as_, -1.0)
+        got = gated(xq, xs, off, w13, s13, aq=aq2.view(F8), as_=as2)
+        assert got[0].data_ptr() == aq2.data_ptr() and got[1].data_ptr() == as2.data_ptr()
+        assert torch.all(aq2[R - 9:] == 0x35) and torch.all(as2[R - 9:] == -1.0)
+        q2, s2 = bi8.silu_mul_quant_fp8(run_grouped(xq, xs, off, w13, s13, variant=bi8.GEMM_TILE_256X128)[: R - 9])
+        assert torch.equal(aq2[: R - 9], q2.view(torch.uint8)) and torch.equal(as2[: R - 9], s2)
+
+
+def test_gated_w13_far_gates_and_non_finite_values():
+    """Gates of -1e2 and beyond (the sigmoid underflows), zero rows, and NaN and infinite activation scales, which
+    stay in their rows, bit for bit as the two calls have them."""
+    I, K = 256, 128
+    xq, xs, off, w13, s13 = grouped_case(77, [40, 50], 2 * I, K)
+    xq[:] = fp8.encode(np.ones((90, K)))
+    w13[:, :I] = fp8.encode(np.full((2, I, K), -1.0))
+    s13[:], xs[:] = 1.0, 1.0
+    xs[:, 0] = np.linspace(0.0, 1.5, 90)      # gates 0 .. -192
+    xs[5, 0], xs[60, 0], xs[61, 0], xs[62, 0] = np.nan, np.inf, -1.0, 0.0
+    h = run_grouped(xq, xs, off, w13, s13, variant=bi8.GEMM_TILE_256X128)
+    want_q, want_s = bi8.silu_mul_quant_fp8(h)
+    aq, as_ = gated(xq, xs, off, w13, s13)
+    a, b = as_.cpu().numpy(), want_s.cpu().numpy()
+    assert np.array_equal(a, b, equal_nan=True)
+    assert np.isnan(a[5]).all() and np.isnan(a[60]).all() and np.isfinite(np.delete(a, [5, 60], 0)).all()
+    fine = np.isfinite(a).all(1)
+    assert np.array_equal(codes_host(aq)[fine], codes_host(want_q)[fine])
+    assert (a[:, 0] > 0).sum() > 20
+
+
 def layer_case(seed, T, E, H, I):
     rng = wl.rng_for(seed)
     x, logits = wl.activations(rng, T, H, 0.01), wl.router_logits(rng, T, E)
@@ -368,7 +420,7 @@ def run_layer(x, logits, w13, s13, w2, s2, k):
 
 
 @pytest.mark.parametrize("T,E,H,I,k", [(1, 2, 128, 128, 1), (3, 8, 256, 144, 2), (40, 3, 384, 256, 2), (257, 5, 256, 400, 4),
-                                       (700, 4, 512, 640, 2)])
+                                       (700, 4, 512, 640, 2), (1200, 3, 640, 1280, 2), (1000, 2, 640, 2048, 2)])
 def test_moe_layer_stage_by_stage(T, E, H, I, k):
     """Every stage against the oracle fed with the stage's own inputs (a sum rounded to the other neighbour
     moves a code by a whole step, so the end of the chain has no tolerance of its own), and the layer
@@ -382,9 +434,14 @@ def test_moe_layer_stage_by_stage(T, E, H, I, k):
     check_product(h, *fp8.moe_gemm_f64(codes_host(xq), xs.cpu().numpy(), off_h, w13, s13), H)
     aq, as_, a = bi8.silu_mul_quant_fp8(h, return_a=True)
     assert_quant(bf16_bits(a), aq, as_)
+    if I % 128 == 0 and bi8.moe_gemm_fp8_select(T * k, 2 * I, H, E) in (bi8.GEMM_TILE_256X128, bi8.GEMM_TILE_256X256):
+        got = bi8.moe_gemm_silu_quant_fp8(xq, xs, off, codes_dev(w13), to_dev(s13))
+        assert torch.equal(got[0].view(torch.uint8), aq.view(torch.uint8)) and torch.equal(got[1], as_)
     want = bits_to_f64(oracle.silu_mul(bf16_bits(h)))
     assert np.all(np.abs(bits_to_f64(bf16_bits(a)) - want) <= np.abs(want) * (2 * 2.0 ** -8 + 2e-5))
-    y2 = bi8.moe_gemm_fp8(aq, as_, off, codes_dev(w2), to_dev(s2))
+    nbytes = bi8.moe_gemm_fp8_workspace_size(T * k, H, I, E)
+    wsp = torch.empty(nbytes, dtype=torch.uint8, device=device()) if nbytes else None
+    y2 = bi8.moe_gemm_fp8(aq, as_, off, codes_dev(w2), to_dev(s2), workspace=wsp)
     check_product(y2, *fp8.moe_gemm_f64(codes_host(aq), as_.cpu().numpy(), off_h, w2, s2), I)
     out = run_layer(*c, k)
     assert torch.equal(out.view(torch.int16), bi8.moe_combine(y2, row_of, weights).view(torch.int16))
@@ -422,8 +479,8 @@ def test_linear_replays_equal_eager(M, N, K):
            lambda r: (bi8.linear_fp8(ins[r], wq, ws, workspace=torch.empty_like(wsp)), *bi8.quant_act_fp8(ins[r])))
 
 
-def test_layer_replays_equal_eager():
-    T, E, H, I, k = 300, 4, 512, 384, 2
+@pytest.mark.parametrize("T,E,H,I,k", [(300, 4, 512, 384, 2), (1200, 3, 640, 1280, 2)])
+def test_layer_replays_equal_eager(T, E, H, I, k):
     cases = [layer_case((82, r), T, E, H, I) for r in range(3)]
     w = [codes_dev(cases[0][2]), to_dev(cases[0][3]), codes_dev(cases[0][4]), to_dev(cases[0][5])]
     ins = [(bf16_to_dev(c[0]), to_dev(c[1])) for c in cases]
