@@ -512,6 +512,54 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// store_tile by way of LDS, for whole lines: a lane's values of one token lie 4
+// columns together, which as stores of 8 bytes to 32 rows an instruction take
+// FILL.  buf: 64 SA SB 32 bytes of this wave's own, free once every wave is here.
+template <int SA, int SB>
+__device__ __forceinline__ void store_lines(const GemmArgs &p, const float (&y)[SA][SB][16], char *buf, int64_t n0,
+                                            int64_t m0, int64_t rows, int ml0, int lane) {
+    constexpr int kPieces = 4 * SA;   // 16-byte pieces of a token's 32 SA values
+    const int rr = lane & 31, hi = lane >> 5;
+    __syncthreads();   // every wave is past its last fragment read
+#pragma unroll
+    for (int b = 0; b < SB; ++b)
+#pragma unroll
+        for (int a = 0; a < SA; ++a)
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = y[a][b][4 * i4 + e];
+                    asm volatile("" : "+v"(v[e]));   // (or the sums would be held as pairs all along, and spill)
+                }
+                if (p.bias) {
+                    const int64_t n = n0 + 32 * a + 8 * i4 + 4 * hi;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
+                }
+                *reinterpret_cast<uint2 *>(buf + ((32 * b + rr) * kPieces + ((4 * a + i4) ^ (rr & (kPieces - 1)))) * 16 +
+                                           8 * hi) =
+                    make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
+            }
+    wave_order();
+    const bool wide = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
+    constexpr int kTokens = 64 / kPieces;   // tokens that a store covers
+#pragma unroll 4
+    for (int j = 0; j < 32 * SB / kTokens; ++j) {
+        const int tok = kTokens * j + lane / kPieces, c = lane & (kPieces - 1);
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(buf + (tok * kPieces + (c ^ (tok & (kPieces - 1)))) * 16);
+        const int64_t n = n0 + 8 * c;
+        if (ml0 + tok >= rows || n >= p.N) continue;
+        uint16_t *dst = p.y + (m0 + ml0 + tok) * p.N + n;
+        if (wide)
+            *reinterpret_cast<u32x4 *>(dst) = v;
+        else
+            store_bf16x8(dst, v, p.N - n);
+    }
+}
+
 // Epilogue of the gated w13 projection: the tile's gate and up columns become the
 // 128 columns t.n0 and on of a = bf16(silu(gate) up), one quantisation group, and
 // leave as codes and scales; gate, up and a are rounded to bf16 where the two
@@ -1142,7 +1190,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     if constexpr (SILU)
         gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), wm, wn == 0, 0, wm * 64, lane);
     else
-        store_tile<SA, SB>(p, y, t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
+        store_lines<SA, SB>(p, y, lds + wave * (SA * SB * 2048), t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1377,7 +1425,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
         gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), 2 * group + (quarter & 1), quarter < 2, 64 * (quarter & 1), group * 64,
                        lane);
     else
-        store_tile<SA, SB>(p, y, t.n0 + quarter * 64, t.m0, t.rows, group * 64, lane);
+        store_lines<SA, SB>(p, y, lds + wave * (SA * SB * 2048), t.n0 + quarter * 64, t.m0, t.rows, group * 64, lane);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
