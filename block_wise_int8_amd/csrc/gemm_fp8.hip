@@ -468,57 +468,23 @@ struct Cfg {
     static_assert(NS >= 3 && NS <= 4, "ring depth");
 };
 
-// Store a wave's SA x SB sub-tiles as bf16, the bias added: weight rows from n0,
-// tile rows from ml0 of the tile at row m0 with `rows` valid rows.  32x32
-// result: lane -> token lane & 31; element i -> weight row 8 (i / 4) + 4 (lane /
-// 32) + i % 4.
-template <int SA, int SB, class Sub>
-__device__ __forceinline__ void store_tile(const GemmArgs &p, const Sub (&y)[SA][SB], int64_t n0, int64_t m0,
-                                           int64_t rows, int ml0, int lane) {
-    const int rr = lane & 31, hi = lane >> 5;
-#pragma unroll
-    for (int b = 0; b < SB; ++b) {
-        const int64_t ml = ml0 + b * 32 + rr;
-        if (ml >= rows) continue;
-        uint16_t *yrow = p.y + (m0 + ml) * p.N;
-#pragma unroll
-        for (int a = 0; a < SA; ++a) {
-#pragma unroll
-            for (int i4 = 0; i4 < 4; ++i4) {
-                const int64_t n = n0 + a * 32 + 8 * i4 + 4 * hi;
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = y[a][b][4 * i4 + e];
-                    if (p.bias && n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
-                }
-                if (p.wide_store) {
-                    if (n < p.N)
-                        *reinterpret_cast<uint2 *>(yrow + n) =
-                            make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < p.N) yrow[n + e] = (uint16_t)(f32x2_to_bf16x2_bits(v[e], 0.0f) & 0xFFFFu);
-                }
-            }
-        }
-    }
-}
-
 // LDS accesses of the wave's lanes stay on their sides of this.
 __device__ __forceinline__ void wave_order() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
 }
 
-// store_tile by way of LDS, for whole lines: a lane's values of one token lie 4
-// columns together, which as stores of 8 bytes to 32 rows an instruction take
-// FILL.  buf: 64 SA SB 32 bytes of this wave's own, free once every wave is here.
-template <int SA, int SB>
-__device__ __forceinline__ void store_lines(const GemmArgs &p, const float (&y)[SA][SB][16], char *buf, int64_t n0,
-                                            int64_t m0, int64_t rows, int ml0, int lane) {
-    constexpr int kPieces = 4 * SA;   // 16-byte pieces of a token's 32 SA values
+// Store a workgroup's tile as bf16, the bias added: BN columns from t.n0, of which a
+// wave's sums start at column col0 and tile row ml0.  32x32 result: lane -> token
+// lane & 31; element i -> weight row 8 (i / 4) + 4 (lane / 32) + i % 4, so a lane
+// has 4 columns together.  Stored from there, 8 bytes to 32 rows an instruction,
+// the tiles of 256 rows took 7 to 9 % longer; by way of LDS whole lines go out (and
+// rows of any N by stores of 16 bytes: N = 5001 47 -> 34 us at 1000 x 5001 x 4096).
+// buf: 2 BN BM bytes, free once every wave is here.
+template <int SA, int SB, int BN, int BM>
+__device__ __forceinline__ void store_lines(const GemmArgs &p, const Tile &t, const float (&y)[SA][SB][16], char *buf,
+                                            int col0, int ml0, int lane, int wave) {
+    constexpr int kPieces = BN / 8;   // 16-byte pieces of a token's values
     const int rr = lane & 31, hi = lane >> 5;
     __syncthreads();   // every wave is past its last fragment read
 #pragma unroll
@@ -534,25 +500,25 @@ __device__ __forceinline__ void store_lines(const GemmArgs &p, const float (&y)[
                     asm volatile("" : "+v"(v[e]));   // (or the sums would be held as pairs all along, and spill)
                 }
                 if (p.bias) {
-                    const int64_t n = n0 + 32 * a + 8 * i4 + 4 * hi;
+                    const int64_t n = t.n0 + col0 + 32 * a + 8 * i4 + 4 * hi;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
                 }
-                *reinterpret_cast<uint2 *>(buf + ((32 * b + rr) * kPieces + ((4 * a + i4) ^ (rr & (kPieces - 1)))) * 16 +
-                                           8 * hi) =
+                const int tok = ml0 + 32 * b + rr, piece = col0 / 8 + 4 * a + i4;
+                *reinterpret_cast<uint2 *>(buf + (tok * kPieces + (piece ^ (tok & 15))) * 16 + 8 * hi) =
                     make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
             }
-    wave_order();
+    __syncthreads();
     const bool wide = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
-    constexpr int kTokens = 64 / kPieces;   // tokens that a store covers
+    constexpr int kTokens = 512 / kPieces;   // tokens that the workgroup stores at once
 #pragma unroll 4
-    for (int j = 0; j < 32 * SB / kTokens; ++j) {
-        const int tok = kTokens * j + lane / kPieces, c = lane & (kPieces - 1);
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(buf + (tok * kPieces + (c ^ (tok & (kPieces - 1)))) * 16);
-        const int64_t n = n0 + 8 * c;
-        if (ml0 + tok >= rows || n >= p.N) continue;
-        uint16_t *dst = p.y + (m0 + ml0 + tok) * p.N + n;
+    for (int j = 0; j < BM / kTokens; ++j) {
+        const int tok = kTokens * j + (64 * wave + lane) / kPieces, c = lane & (kPieces - 1);
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(buf + (tok * kPieces + (c ^ (tok & 15))) * 16);
+        const int64_t n = t.n0 + 8 * c;
+        if (tok >= t.rows || n >= p.N) continue;
+        uint16_t *dst = p.y + (t.m0 + tok) * p.N + n;
         if (wide)
             *reinterpret_cast<u32x4 *>(dst) = v;
         else
@@ -936,7 +902,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
             return;
         }
     }
-    store_tile<SA, SB>(p, y, t.n0 + wn * C::kWaveN, t.m0, t.rows, wm * C::kWaveM, lane);
+    store_lines<SA, SB, C::kBN, C::kBM>(p, t, y, lds, wn * C::kWaveN, wm * C::kWaveM, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1190,7 +1156,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     if constexpr (SILU)
         gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), wm, wn == 0, 0, wm * 64, lane);
     else
-        store_lines<SA, SB>(p, y, lds + wave * (SA * SB * 2048), t.n0 + wn * 128, t.m0, t.rows, wm * 64, lane);
+        store_lines<SA, SB, C::kBN, C::kBM>(p, t, y, lds, wn * 128, wm * 64, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1425,7 +1391,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
         gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), 2 * group + (quarter & 1), quarter < 2, 64 * (quarter & 1), group * 64,
                        lane);
     else
-        store_lines<SA, SB>(p, y, lds + wave * (SA * SB * 2048), t.n0 + quarter * 64, t.m0, t.rows, group * 64, lane);
+        store_lines<SA, SB, C::kBN, C::kBM>(p, t, y, lds, quarter * 64, group * 64, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
