@@ -122,19 +122,19 @@ def _check(status: int) -> None:
 
 
 def _stream_handle(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be on a HIP device (got %s); there is no CPU path" % (name, t.device))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     if t.dim() != ndim:
         raise ValueError("%s must have %d dims (got shape %s)" % (name, ndim, tuple(t.shape)))
