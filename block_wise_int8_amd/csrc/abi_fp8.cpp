@@ -127,6 +127,52 @@ int32_t rmsnorm_quant(const char *fn, bool fp8, const uint16_t *x, int64_t ldx, 
                                                           xs, static_cast<hipStream_t>(stream)));
 }
 
+// The layer's workspace: parts at multiples of 256 bytes.  The w13 GEMM's output
+// and the w2 GEMM's share one (the first is read before the second is written).
+struct LayerPlan {
+    bool gated;   // w13 and the gating in one launch
+    int64_t ids, weights, sorted_token, offsets, row_of, xq, xs, h, aq, as, partial, partial_bytes, bytes;
+    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+        const int64_t R = T * k, HB = (H + 127) / 128, IB = (I + 127) / 128;
+        const bi8::Fp8Path path = bi8::select_moe_gemm_fp8_path(R, 2 * I, H, E);
+        gated = I % 128 == 0 && (path == bi8::Fp8Path::kTile256x128 || path == bi8::Fp8Path::kTile256x256);
+        const int64_t p13 = gated ? 0 : bi8::moe_gemm_fp8_workspace_bytes(R, 2 * I, H, E);
+        const int64_t p2 = bi8::moe_gemm_fp8_workspace_bytes(R, H, I, E);
+        partial_bytes = p13 > p2 ? p13 : p2;
+        const int64_t wide = !gated && 2 * I > H ? 2 * I : H;
+        bytes = 0;
+        auto take = [this](int64_t n) {
+            const int64_t at = bytes;
+            bytes += (n + 255) / 256 * 256;
+            return at;
+        };
+        ids = take(R * 4);
+        weights = take(R * 4);
+        sorted_token = take(R * 4);
+        offsets = take((E + 1) * 4);
+        row_of = take(R * 4);
+        xq = take(R * H);
+        xs = take(R * HB * 4);
+        h = take(R * wide * 2);
+        aq = take(R * I);
+        as = take(R * IB * 4);
+        partial = take(partial_bytes);
+    }
+};
+
+int32_t check_layer(const char *fn, int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+    if (E < 1 || E > 1024) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 1024]", fn, E);
+    if (k < 1 || k > 8 || k > E) return fail_status(BI8_ERR_SHAPE, "%s: k = %d out of range [1, min(E, 8)]", fn, k);
+    if (T < 0 || T > kMaxRows / k)
+        return fail_status(BI8_ERR_SHAPE, "%s: T = %lld out of range", fn, (long long)T);
+    BI8_TRY(check_columns(fn, "H", H));
+    BI8_TRY(check_columns(fn, "I", I));
+    if (H % 16 != 0 || I % 16 != 0)
+        return fail_status(BI8_ERR_ALIGN, "%s: H = %lld and I = %lld must be multiples of 16", fn, (long long)H,
+                           (long long)I);
+    return BI8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -306,6 +352,64 @@ int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, i
         E > 65536)
         return 0;
     return bi8::moe_gemm_fp8_workspace_bytes(R, N, K, E);
+}
+
+int64_t blockint8_moe_layer_fp8_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+    if (E < 1 || E > 1024 || k < 1 || k > 8 || k > E || T <= 0 || T > kMaxRows / k || H <= 0 || H > BI8_MAX_K ||
+        H % 16 != 0 || I <= 0 || I > BI8_MAX_K || I % 16 != 0)
+        return 0;
+    return LayerPlan(T, H, I, E, k).bytes;
+}
+
+int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *logits, const uint8_t *w13,
+                                const float *ws13, const uint8_t *w2, const float *ws2, uint16_t *out, int64_t T,
+                                int64_t H, int64_t I, int32_t E, int32_t k, int32_t renormalize, int32_t block_n,
+                                int32_t block_k, void *workspace, int64_t workspace_bytes, void *stream) {
+    static const char fn[] = "blockint8_moe_layer_fp8";
+    BI8_TRY(check_layer(fn, T, H, I, E, k));
+    BI8_TRY(check_pitch(fn, "ldx", ldx, H));
+    BI8_TRY(check_block(fn, block_n, block_k));
+    if (T == 0) return done(fn);
+    if (!x || !logits || !w13 || !ws13 || !w2 || !ws2 || !out || !workspace) return null_pointer(fn);
+    BI8_TRY(check_align(fn, "x", x, 2));
+    BI8_TRY(check_align(fn, "logits", logits, 4));
+    BI8_TRY(check_align(fn, "w13", w13, 16));
+    BI8_TRY(check_align(fn, "ws13", ws13, 4));
+    BI8_TRY(check_align(fn, "w2", w2, 16));
+    BI8_TRY(check_align(fn, "ws2", ws2, 4));
+    BI8_TRY(check_align(fn, "out", out, 16));
+    BI8_TRY(check_align(fn, "workspace", workspace, 256));
+    const LayerPlan p(T, H, I, E, k);
+    if (workspace_bytes < p.bytes)
+        return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
+                           (long long)p.bytes);
+    char *const at = static_cast<char *>(workspace);
+    auto i32 = [at](int64_t off) { return reinterpret_cast<int32_t *>(at + off); };
+    auto f32 = [at](int64_t off) { return reinterpret_cast<float *>(at + off); };
+    auto u8 = [at](int64_t off) { return reinterpret_cast<uint8_t *>(at + off); };
+    uint16_t *const h = reinterpret_cast<uint16_t *>(at + p.h);
+    float *const partial = p.partial_bytes ? f32(p.partial) : nullptr;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t R = T * k;
+    hipError_t e = bi8::launch_moe_route(logits, T, E, k, renormalize, i32(p.ids), f32(p.weights), i32(p.sorted_token),
+                                         i32(p.offsets), i32(p.row_of), st);
+    if (e == hipSuccess)
+        e = bi8::launch_quant_act_fp8(x, T, ldx, i32(p.sorted_token), R, H, u8(p.xq), f32(p.xs), st);
+    if (p.gated) {
+        if (e == hipSuccess)
+            e = bi8::launch_moe_gemm_silu_quant_fp8(u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, u8(p.aq), f32(p.as),
+                                                    R, I, H, E, st);
+    } else {
+        if (e == hipSuccess)
+            e = bi8::launch_moe_gemm_fp8(bi8::Fp8Path::kAuto, u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, h, R,
+                                         2 * I, H, E, partial, p.partial_bytes, st);
+        if (e == hipSuccess) e = bi8::launch_silu_mul_quant_fp8(h, R, I, u8(p.aq), f32(p.as), nullptr, st);
+    }
+    if (e == hipSuccess)
+        e = bi8::launch_moe_gemm_fp8(bi8::Fp8Path::kAuto, u8(p.aq), f32(p.as), i32(p.offsets), w2, ws2, h, R, H, I, E,
+                                     partial, p.partial_bytes, st);
+    if (e == hipSuccess) e = bi8::launch_moe_combine(h, R, i32(p.row_of), f32(p.weights), T, k, H, out, st);
+    return bi8::call_status(fn, e);
 }
 
 int32_t blockint8_rmsnorm_quant(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,

@@ -13,8 +13,8 @@ from . import _call as c
 
 __all__ = ["quant_act_fp8", "quant_act_gather_fp8", "silu_mul_quant_fp8", "quant_weight_fp8", "gemm_fp8",
            "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_silu_quant_fp8",
-           "moe_gemm_fp8_workspace_size", "gemm_fp8_select",
-           "moe_gemm_fp8_select", "moe_layer_fp8", "GEMM_TILE_128X128"]
+           "moe_gemm_fp8_workspace_size", "gemm_fp8_select", "moe_gemm_fp8_select", "moe_layer_fp8",
+           "moe_layer_fp8_workspace_size", "GEMM_TILE_128X128"]
 
 FP8 = torch.float8_e4m3fn
 GEMM_TILE_128X128 = 5   # the kernel variant that the int8 GEMM does not have
@@ -31,6 +31,9 @@ def declare(lib) -> None:
     c.declare(lib, "blockint8_linear_fp8", [vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, i64, vp])
     c.declare(lib, "blockint8_moe_gemm_fp8", [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, i64, vp])
     c.declare(lib, "blockint8_moe_gemm_silu_quant_fp8", [vp] * 7 + [i64, i64, i64, i32, i32, i32, vp])
+    c.declare(lib, "blockint8_moe_layer_fp8", [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, vp,
+                                               i64, vp])
+    c.declare(lib, "blockint8_moe_layer_fp8_workspace_size", [i64, i64, i64, i32, i32], i64)
     c.declare(lib, "blockint8_gemm_fp8_variant", [i32] + lib.blockint8_gemm_fp8.argtypes)
     c.declare(lib, "blockint8_moe_gemm_fp8_variant", [i32] + lib.blockint8_moe_gemm_fp8.argtypes)
     c.declare(lib, "blockint8_gemm_fp8_select", [i64, i64, i64])
@@ -220,29 +223,42 @@ def moe_gemm_silu_quant_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: 
     return aq, as_
 
 
+def moe_layer_fp8_workspace_size(T: int, H: int, I: int, E: int, k: int) -> int:
+    """Bytes of workspace ``moe_layer_fp8`` needs for T tokens."""
+    return int(_bi8.load().blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k))
+
+
 def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor, w2: torch.Tensor,
-                  ws2: torch.Tensor, k: int, renormalize: bool = False) -> torch.Tensor:
-    """The e4m3 FusedMoE layer on the GPU: route, gather + quantise, w13 grouped
-    GEMM, SiLU gating + quantise, w2 grouped GEMM, weighted combine.  Where the
-    w13 GEMM runs 256-row weight tiles and I % 128 == 0, it and the gating are
-    one launch (moe_gemm_silu_quant_fp8).  x bf16 [T, H]; logits fp32 [T, E];
-    w13 float8_e4m3fn [E, 2I, H]; w2 float8_e4m3fn [E, H, I].  Returns bf16 [T, H]."""
+                  ws2: torch.Tensor, k: int, renormalize: bool = False, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The e4m3 FusedMoE layer on the GPU, through one C call: route, gather +
+    quantise, w13 grouped GEMM, SiLU gating + quantise, w2 grouped GEMM,
+    weighted combine.  Where the w13 GEMM runs 256-row weight tiles and
+    I % 128 == 0, it and the gating are one launch (moe_gemm_silu_quant_fp8).
+    x bf16 [T, H]; logits fp32 [T, E]; w13 float8_e4m3fn [E, 2I, H]; w2
+    float8_e4m3fn [E, H, I]; H and I multiples of 16.  ``workspace``: any
+    contiguous tensor on the device of ``moe_layer_fp8_workspace_size`` bytes
+    or more (a fresh one when not given); calls that share one must not
+    overlap in time.  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
-    with torch.cuda.device(dev):
-        _, weights, sorted_token, offsets, row_of = _bi8.moe_route(logits, k, renormalize)
-        xq, xs = quant_act_gather_fp8(x, sorted_token)
-        R, H = xq.shape
-        E, N = w13.shape[:2]
-        if N % 256 == 0 and moe_gemm_fp8_select(R, N, H, E) in (_bi8.GEMM_TILE_256X128, _bi8.GEMM_TILE_256X256):
-            aq, as_ = moe_gemm_silu_quant_fp8(xq, xs, offsets, w13, ws13)
-        else:
-            wsp = _layer_workspace(R, N, H, E, dev)
-            aq, as_ = silu_mul_quant_fp8(moe_gemm_fp8(xq, xs, offsets, w13, ws13, workspace=wsp))
-        wsp = _layer_workspace(R, w2.shape[1], aq.shape[1], E, dev)
-        y2 = moe_gemm_fp8(aq, as_, offsets, w2, ws2, workspace=wsp)
-        return _bi8.moe_combine(y2, row_of, weights)
-
-
-def _layer_workspace(R: int, N: int, K: int, E: int, dev: int):
-    nbytes = moe_gemm_fp8_workspace_size(R, N, K, E)
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    T, H, ldx = c.rows(x, "x", dev)
+    c.dense(logits, "logits", dev, torch.float32, (T, None))
+    E = logits.shape[1]
+    c.dense(w13, "w13", dev, FP8, (E, None, H))
+    N = w13.shape[1]
+    if N % 2:
+        raise ValueError("w13 must have an even number of rows (gate, then up)")
+    I = N // 2
+    c.dense(ws13, "ws13", dev, torch.float32, (E, _blocks(N), _blocks(H)))
+    c.dense(w2, "w2", dev, FP8, (E, H, I))
+    c.dense(ws2, "ws2", dev, torch.float32, (E, _blocks(H), _blocks(I)))
+    out = c.output(out, "out", dev, torch.bfloat16, (T, H))
+    lib = _bi8.load()
+    if workspace is None:
+        workspace = torch.empty(lib.blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k), dtype=torch.uint8,
+                                device=dev)
+    wsp, nbytes = c.scratch(workspace, dev)
+    _bi8._check(c.call(lib.blockint8_moe_layer_fp8, dev, x.data_ptr(), ldx, logits.data_ptr(), w13.data_ptr(),
+                       ws13.data_ptr(), w2.data_ptr(), ws2.data_ptr(), out.data_ptr(), T, H, I, E, k,
+                       1 if renormalize else 0, 128, 128, wsp, nbytes))
+    return out

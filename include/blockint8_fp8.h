@@ -162,6 +162,38 @@ int32_t blockint8_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, co
                                           void *stream);
 
 /*
+ * The whole MoE layer in one call, six or seven launches on the stream:
+ * blockint8_moe_route of the logits, blockint8_quant_act_gather_fp8, the w13
+ * GEMM with the gating (blockint8_moe_gemm_silu_quant_fp8 where the grouped GEMM
+ * of that size runs 256 x 128 or 256 x 256 tiles and I % 128 == 0, else
+ * blockint8_moe_gemm_fp8 and blockint8_silu_mul_quant_fp8), the w2 GEMM and
+ * blockint8_moe_combine.  out equals those calls' exactly.
+ *
+ *   x       bf16 [T, ldx], the first H columns of each row (2-byte aligned)
+ *   logits  fp32 [T, E]
+ *   w13     e4m3 [E, 2 I, H]   ws13  fp32 [E, ceil(2 I / 128), ceil(H / 128)]
+ *   w2      e4m3 [E, H, I]     ws2   fp32 [E, ceil(H / 128), ceil(I / 128)]
+ *   out     bf16 [T, H]   (output, 16-byte aligned)
+ *   workspace        device memory, 256-byte aligned, of at least
+ *                    blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k)
+ *                    bytes; contents undefined before and after.  Calls that
+ *                    share one must not overlap in time.
+ *
+ * Limits: 1 <= E <= 1024, 1 <= k <= min(E, 8), H and I multiples of 16,
+ * T * k < 2^31.  Errors: NULL pointer (T > 0) -> BI8_ERR_NULL; a limit broken,
+ * ldx < H or a workspace too small -> BI8_ERR_SHAPE; blocks other than [128,
+ * 128] -> BI8_ERR_BLOCK; H % 16, I % 16 or a pointer's alignment ->
+ * BI8_ERR_ALIGN.
+ */
+int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *logits, const uint8_t *w13,
+                                const float *ws13, const uint8_t *w2, const float *ws2, uint16_t *out, int64_t T,
+                                int64_t H, int64_t I, int32_t E, int32_t k, int32_t renormalize, int32_t block_n,
+                                int32_t block_k, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* 0 for sizes that blockint8_moe_layer_fp8 rejects, and for T = 0. */
+int64_t blockint8_moe_layer_fp8_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
+
+/*
  * Kernel variants, as in blockint8.h: the *_select functions tell which kernel
  * blockint8_gemm_fp8 / blockint8_moe_gemm_fp8 choose for a size without a
  * workspace, the *_variant forms run a named one (which leaves the workspace

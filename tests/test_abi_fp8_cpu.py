@@ -27,6 +27,8 @@ CALLS = {
                          nbytes=0),
     "moe_gemm_silu_quant_fp8": dict(xq=P, xs=P, off=P, w13=P, ws13=P, aq=P, as_=P, R=4, I=256, K=256, E=2, bn=128,
                                     bk=128),
+    "moe_layer_fp8": dict(x=P, ldx=256, logits=P, w13=P, ws13=P, w2=P, ws2=P, out=P, T=4, H=256, I=256, E=8, k=2, renorm=0,
+                          bn=128, bk=128, wsp=P, nbytes=1 << 30),
     "rmsnorm_quant": dict(x=P, ldx=256, residual=P, ldr=256, weight=P, eps=1e-6, M=4, H=256, bk=128, h=P, ldh=256,
                           y=None, xq=P, xs=P),
 }
@@ -79,6 +81,13 @@ BAD = {
         (dict(K=0), SHAPE), (dict(K=100), ALIGN), (dict(E=0), SHAPE), (dict(E=65537), SHAPE), (dict(bn=64), BLOCK),
         (dict(bk=64), BLOCK), (dict(off=P + 2), ALIGN), (dict(xq=P + 8), ALIGN), (dict(xs=P + 2), ALIGN),
         (dict(w13=P + 8), ALIGN), (dict(ws13=P + 2), ALIGN), (dict(aq=P + 8), ALIGN), (dict(as_=P + 2), ALIGN)],
+    "moe_layer_fp8": [(dict([(name, None)]), NULL) for name in ("x", "logits", "w13", "ws13", "w2", "ws2", "out", "wsp")] + [
+        (dict(T=-1), SHAPE), (dict(T=1 << 30), SHAPE), (dict(H=0), SHAPE), (dict(I=0), SHAPE), (dict(E=0), SHAPE),
+        (dict(H=1 << 24, ldx=1 << 24), SHAPE), (dict(I=1 << 24), SHAPE), (dict(E=1025), SHAPE), (dict(k=0), SHAPE),
+        (dict(k=9), SHAPE), (dict(E=1), SHAPE), (dict(ldx=255), SHAPE), (dict(nbytes=0), SHAPE), (dict(nbytes=-1), SHAPE),
+        (dict(nbytes=4096), SHAPE), (dict(H=248), ALIGN), (dict(I=40), ALIGN), (dict(bn=64), BLOCK), (dict(bk=1), BLOCK),
+        (dict(x=ODD), ALIGN), (dict(logits=P + 2), ALIGN), (dict(w13=P + 8), ALIGN), (dict(ws13=P + 2), ALIGN),
+        (dict(w2=P + 8), ALIGN), (dict(ws2=P + 2), ALIGN), (dict(out=P + 8), ALIGN), (dict(wsp=P + 128), ALIGN)],
     "rmsnorm_quant": NORM_BAD, "rmsnorm_quant_fp8": NORM_BAD,
 }
 
@@ -97,7 +106,7 @@ def test_refusals(name, kw, status):
 
 @pytest.mark.parametrize("name", sorted(CALLS))
 def test_empty_is_a_no_op(name):
-    size = next(k for k in ("M", "R", "N") if k in CALLS[name])
+    size = next(k for k in ("M", "R", "N", "T") if k in CALLS[name])
     none = {k: None for k, v in CALLS[name].items() if v == P}
     assert run(name, **{**none, size: 0}) == OK
     assert bi8.load().blockint8_last_error().decode() == ""
@@ -128,6 +137,10 @@ def test_variant_rules():
 
 def test_workspace_sizes_of_bad_problems_are_zero():
     assert bi8.gemm_fp8_workspace_size(0, 10, 10) == 0 and bi8.gemm_fp8_workspace_size(10, -1, 10) == 0
+    for bad in ((0, 256, 256, 8, 2), (4, 250, 256, 8, 2), (4, 256, 24, 8, 2), (4, 256, 256, 8, 9), (4, 256, 256, 0, 1),
+                (1 << 31, 256, 256, 8, 2), (4, 256, 0, 8, 2), (4, 256, 256, 2, 3)):
+        assert bi8.moe_layer_fp8_workspace_size(*bad) == 0
+    assert bi8.moe_layer_fp8_workspace_size(4, 256, 256, 8, 2) > 4 * 2 * 256 * 4
     assert bi8.moe_gemm_fp8_workspace_size(8, 10, 100, 2) == 0 and bi8.moe_gemm_fp8_workspace_size(8, 10, 128, 0) == 0
 
 

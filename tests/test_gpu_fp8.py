@@ -443,8 +443,21 @@ def test_moe_layer_stage_by_stage(T, E, H, I, k):
     wsp = torch.empty(nbytes, dtype=torch.uint8, device=device()) if nbytes else None
     y2 = bi8.moe_gemm_fp8(aq, as_, off, codes_dev(w2), to_dev(s2), workspace=wsp)
     check_product(y2, *fp8.moe_gemm_f64(codes_host(aq), as_.cpu().numpy(), off_h, w2, s2), I)
-    out = run_layer(*c, k)
-    assert torch.equal(out.view(torch.int16), bi8.moe_combine(y2, row_of, weights).view(torch.int16))
+    want = bi8.moe_combine(y2, row_of, weights)
+    assert torch.equal(run_layer(*c, k).view(torch.int16), want.view(torch.int16))
+    # rows of a wider buffer, the caller's output, and a workspace with anything in it, guarded behind its end
+    wide = torch.full((T, H + 24), 7.0, dtype=torch.bfloat16, device=device())
+    wide[:, :H] = bf16_to_dev(x)
+    nbytes = bi8.moe_layer_fp8_workspace_size(T, H, I, E, k)
+    wsp = torch.full((nbytes + 4096,), 0xFF, dtype=torch.uint8, device=device())
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=device())
+    got = bi8.moe_layer_fp8(wide[:, :H], to_dev(logits), codes_dev(w13), to_dev(s13), codes_dev(w2), to_dev(s2), k, out=out,
+                            workspace=wsp[:nbytes])
+    assert got is out and torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert torch.all(wsp[nbytes:] == 0xFF)
+    _, weights, _, _, _ = bi8.moe_route(to_dev(logits), k, True)
+    got = bi8.moe_layer_fp8(bf16_to_dev(x), to_dev(logits), codes_dev(w13), to_dev(s13), codes_dev(w2), to_dev(s2), k, True)
+    assert torch.equal(got.view(torch.int16), bi8.moe_combine(y2, row_of, weights).view(torch.int16))
 
 
 # --------------------------------------------- graphs, streams, other calls --
@@ -529,8 +542,33 @@ def test_binding_refusals():
         (ValueError, lambda: bi8.moe_gemm_fp8(xq, s, torch.zeros(2, dtype=torch.int32, device=dev), w[None].repeat(2, 1, 1), ws[None].repeat(2, 1, 1))),
         (bi8.BlockInt8Error, lambda: bi8.gemm_fp8(xq, s, w, ws, workspace=torch.empty(64, dtype=torch.uint8, device=dev)[1:])),
     ]
+    off = torch.zeros(3, dtype=torch.int32, device=dev)
+    logits = torch.zeros(4, 2, device=dev)
+    w13, s13 = torch.zeros(2, 512, 256, dtype=F8, device=dev), torch.zeros(2, 4, 2, device=dev)
+    w2, s2 = torch.zeros(2, 256, 256, dtype=F8, device=dev), torch.zeros(2, 2, 2, device=dev)
+    layer = lambda **kw: bi8.moe_layer_fp8(*{**dict(x=x, logits=logits, w13=w13, ws13=s13, w2=w2, ws2=s2, k=2), **kw}.values())
+    bad += [
+        (ValueError, lambda: bi8.moe_gemm_silu_quant_fp8(xq, s, off[:2], w13, s13)),
+        (ValueError, lambda: bi8.moe_gemm_silu_quant_fp8(xq, s, off, w13[:, :511], s13)),
+        (ValueError, lambda: bi8.moe_gemm_silu_quant_fp8(xq, s, off, w13, s13, aq=xq[:, :128])),
+        (bi8.BlockInt8Error, lambda: bi8.moe_gemm_silu_quant_fp8(
+            xq, s, off, w13[:, :288].contiguous(), s13[:, :3].contiguous())),         # I = 144
+        (ValueError, lambda: layer(logits=logits[:3])),
+        (TypeError, lambda: layer(logits=logits.double())),
+        (ValueError, lambda: layer(w13=w13[:1])),
+        (ValueError, lambda: layer(w13=w13[:, :511])),
+        (ValueError, lambda: layer(ws13=s13[:, :2])),
+        (ValueError, lambda: layer(w2=w2[:, :128])),
+        (ValueError, lambda: layer(ws2=s2[:1])),
+        (ValueError, lambda: layer(x=x[:, :128])),
+        (bi8.BlockInt8Error, lambda: layer(k=0)),
+        (bi8.BlockInt8Error, lambda: layer(k=3)),
+        (ValueError, lambda: layer(renormalize=False, out=torch.empty(4, 128, dtype=torch.bfloat16, device=dev))),
+        (bi8.BlockInt8Error, lambda: layer(renormalize=False, out=None, workspace=torch.empty(256, device=dev))),
+    ]
     for error, fn in bad:
         with pytest.raises(error):
             fn()
+    assert torch.equal(layer(), torch.zeros_like(x)) and layer(x=x[:0], logits=logits[:0]).shape == (0, 256)
     assert bi8.gemm_fp8(xq[:0], s[:0], w, ws).shape == (0, 8)
     assert bi8.quant_act_fp8(x[:0])[0].shape == (0, 256)
