@@ -10,10 +10,12 @@
 // of 2^3 counts and one of 2^2 does not; the older 16x16x32 form does the
 // same), and those sums in fp32.  That is 7 2^-13 of the largest product of the
 // eight at most, against the 2^-4 to which each code was rounded; the bf16
-// product of the converted codes would avoid it at half the rate.  The weight rows are the A operand (rows of
-// the result = output columns n) and the activation rows the B operand
-// (columns = tokens m), so that a lane holds one token and columns of one
-// 128-row weight block: the scale xs[m, g] ws[n / 128, g] is one factor a lane.
+// product of the converted codes would avoid it at half the rate.
+//
+// The weight rows are the A operand (rows of the result = output columns n) and
+// the activation rows the B operand (columns = tokens m), so that a lane holds
+// one token and columns of one 128-row weight block: the scale xs[m, g]
+// ws[n / 128, g] is one factor a lane.
 // K may be permuted inside a block as long as both operands agree, so a
 // lane's 32 operand bytes are whichever two 16-byte pieces are cheapest to
 // bring there.
@@ -45,8 +47,9 @@ __device__ __forceinline__ i32x8 join16(i32x4 a, i32x4 b) {
 // load of U blocks is issued before the first MFMA, and the parts' sums meet
 // in LDS.
 //
-// Measured (weights from HBM): 8 x 4096 x 4096 7.2 us; grouped, 16 rows over 8
-// experts of 28672 x 4096 (940 MB) 148 us, 6.35 TB/s.
+// Measured (weights from HBM): 1 x 131072 x 4096 102 us, 5.3 TB/s; 8 x 4096 x
+// 4096 7.3 us, most of it one workgroup's latency; grouped, 16 rows over 8
+// experts of 28672 x 4096 (940 MB, read once by the counters) 137 to 149 us.
 //
 // Rows [a, b) of the activations share the weight; they are taken 16 MT at a
 // time.  Dense: [0, M), chunks over blockIdx.y.  MOE: one expert's segment, all
@@ -366,7 +369,8 @@ __global__ __launch_bounds__(256) void moe_fp8_tail_reduce_kernel(GemmArgs p) {
         const int64_t n = t.n0 + c;
         if (c >= BN || n >= p.N) continue;
         f32x4 acc = *reinterpret_cast<const f32x4 *>(slots + c);
-        for (int32_t z = 1; z < tp.splits; ++z) acc += *reinterpret_cast<const f32x4 *>(slots + (int64_t)z * (BM * BN) + c);
+        for (int32_t z = 1; z < tp.splits; ++z)
+            acc += *reinterpret_cast<const f32x4 *>(slots + (int64_t)z * (BM * BN) + c);
         if (p.wide_store) {
             *reinterpret_cast<uint2 *>(yrow + n) =
                 make_uint2(f32x2_to_bf16x2_bits(acc[0], acc[1]), f32x2_to_bf16x2_bits(acc[2], acc[3]));
@@ -445,6 +449,11 @@ __device__ __forceinline__ void wait_lds() {
 // rescaled behind the next one's MFMAs.  One barrier a block.
 // The activation scales reach LDS eight blocks at a time; the weight scale of
 // a wave's 128-row block is a scalar load a block ahead.
+//
+// Bound by that chain: 0.5 us a block with 128 x 64 tiles, whose MFMAs take a
+// quarter of it.  Measured (us): 128 x 64 333 x 5000 x 4000 21.9, 512 x 4096 x
+// 4096 18.1; 128 x 128 1024 x 4096 x 4096 25.5, grouped 512 x 4096 x 14336 over 8
+// experts 97.
 template <int WN_, int WM_, int SA_, int SB_, int NS_>
 struct Cfg {
     static constexpr int WN = WN_, WM = WM_, SA = SA_, SB = SB_, NS = NS_;
@@ -629,7 +638,8 @@ __device__ __forceinline__ void gate_store(const GemmArgs &p, const Tile &t, con
 #pragma unroll
     for (int j = 0; j < 32 / kTokens; ++j) {
         const int tok = kTokens * j + lane / kPieces, c = lane & (kPieces - 1);
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(gates + tok * (kPieces * 16) + (c ^ (tok & (kPieces - 1))) * 16);
+        const i32x4 v =
+            *reinterpret_cast<const i32x4 *>(gates + tok * (kPieces * 16) + (c ^ (tok & (kPieces - 1))) * 16);
         if (ml + tok < t.rows)
             *reinterpret_cast<i32x4 *>(p.aq + (t.m0 + ml + tok) * p.I + t.n0 + col0 + 16 * c) = v;
     }
@@ -713,7 +723,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
         for (int j = 0; j < C::kLoads; ++j) {
             const bool weight = j < C::kWLoads;
             const int q = wave + (weight ? j : j - C::kWLoads) * C::kWaves;
-            *reinterpret_cast<i32x4 *>(lds + st * C::kStageBytes + (weight ? 0 : C::kXOff) + q * 1024 + lane * 16) = held[j];
+            *reinterpret_cast<i32x4 *>(lds + st * C::kStageBytes + (weight ? 0 : C::kXOff) + q * 1024 + lane * 16) =
+                held[j];
         }
     };
     auto fill = [&](const int st, int kb) __attribute__((always_inline)) {
@@ -921,6 +932,14 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
 // kb + 2 as soon as both groups have read those of kb into registers, the
 // weight sub-rows a cluster or two after they were read, so that fills run
 // between one and two blocks ahead and no wait drains them.
+//
+// Bound by the matrix core at the clock that the power cap leaves: 2048 x 28672 x
+// 4096 227 us, 2120 TFLOP/s, the matrix core busy 68 % of the time at 1.8 GHz (of
+// 2.4); 8192^3 445 us; grouped, 8192 rows over 8 experts of 28672 x 4096 971 us.
+// Of a tile's 57 us at K = 4096 about 4 go on its first fills and 4 on its stores.
+// (A workgroup that walked several tiles, filling the next one's first blocks
+// during the last of the one before, lost more on the bookkeeping in its
+// loop: 8192^3 488 us, 2048 x 28672 x 4096 245.)
 struct PingPong {
     static constexpr int kThreads = 512;
     static constexpr int kBN = 256, kBM = 256, SA = 4, SB = 2;
@@ -1163,7 +1182,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
 // The same for 256 x 128 tiles, where 256 x 256 would leave CUs without a tile or
 // pad short segments: waves of 64 weight rows x 64 activation rows, group g
 // owning activation rows 64 g, a block of two clusters, and three whole stages
-// of 48 KB.
+// of 48 KB.  Measured: 2048 x 4096 x 14336 117 us, 2060 TFLOP/s; grouped, 512 rows
+// over 8 experts of 28672 x 4096 192 us, there bound by the weight's stream (949 MB
+// by the counters, 4.9 TB/s).
 struct PingPong128 {
     static constexpr int kThreads = 512;
     static constexpr int kBN = 256, kBM = 128, SA = 2, SB = 2;
@@ -1388,8 +1409,8 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     wait_vmcnt<0>();   // no LDS fill may outlive the workgroup
 
     if constexpr (SILU)
-        gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), 2 * group + (quarter & 1), quarter < 2, 64 * (quarter & 1), group * 64,
-                       lane);
+        gate_store<SA>(p, t, y, lds, reinterpret_cast<uint32_t *>(xsl), 2 * group + (quarter & 1), quarter < 2,
+                       64 * (quarter & 1), group * 64, lane);
     else
         store_lines<SA, SB, C::kBN, C::kBM>(p, t, y, lds, quarter * 64, group * 64, lane, wave);
 #endif  // __HIP_DEVICE_COMPILE__

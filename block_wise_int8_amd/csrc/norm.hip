@@ -15,6 +15,9 @@
 // Bound by HBM: 2 B read an element (4 with the residual) and 1 B written (2
 // more for h, 2 more for the optional bf16 y), 4 B a group.  A row stays in
 // registers as bf16 between the sum and the codes, so it is read once.
+// Measured with a residual and e4m3 codes: 1 x 4096 3.2 us (a launch's latency),
+// 4096 x 4096 22 us (5.3 TB/s), 16384 x 4096 82 us (5.7), 2048 x 20000, walked
+// twice, 64 us.
 #include "codes.hpp"
 #include "internal.hpp"
 

@@ -236,10 +236,10 @@ def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13
     weighted combine.  Where the w13 GEMM runs 256-row weight tiles and
     I % 128 == 0, it and the gating are one launch (moe_gemm_silu_quant_fp8).
     x bf16 [T, H]; logits fp32 [T, E]; w13 float8_e4m3fn [E, 2I, H]; w2
-    float8_e4m3fn [E, H, I]; H and I multiples of 16.  ``workspace``: any
-    contiguous tensor on the device of ``moe_layer_fp8_workspace_size`` bytes
-    or more (a fresh one when not given); calls that share one must not
-    overlap in time.  Returns bf16 [T, H]."""
+    float8_e4m3fn [E, H, I]; H and I multiples of 16.  ``workspace``: a
+    contiguous, 256-byte aligned tensor of any type on the device, of
+    ``moe_layer_fp8_workspace_size`` bytes or more (a fresh one when not
+    given); calls that share one must not overlap in time.  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
     T, H, ldx = c.rows(x, "x", dev)
     c.dense(logits, "logits", dev, torch.float32, (T, None))
