@@ -423,6 +423,10 @@ __device__ __forceinline__ i32x4 load_piece(const int8_t *p, int64_t n) {
     return v;
 }
 
+// Where a row's scale of block b of a batch of 8 lies among the row's 8: 32 rows'
+// scales of one block in 32 banks.
+__device__ __forceinline__ int scale_slot(int b, int row) { return b ^ ((row >> 2) & 7); }
+
 // Wait until at most N buffer-to-LDS fills are in flight (63: any number) and
 // every LDS read has returned.
 template <int N>
@@ -515,7 +519,9 @@ __device__ __forceinline__ void store_lines(const GemmArgs &p, const Tile &t, co
                         if (n + e < p.N) v[e] += bf16_bits_to_f32(p.bias[n + e]);
                 }
                 const int tok = ml0 + 32 * b + rr, piece = col0 / 8 + 4 * a + i4;
-                *reinterpret_cast<uint2 *>(buf + (tok * kPieces + (piece ^ (tok & 15))) * 16 + 8 * hi) =
+                // (tokens 16 to 31 with the halves of a piece exchanged: the 8 bytes of
+                // 32 tokens lie in 64 banks)
+                *reinterpret_cast<uint2 *>(buf + (tok * kPieces + (piece ^ (tok & 15))) * 16 + 8 * (hi ^ ((rr >> 4) & 1))) =
                     make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
             }
     __syncthreads();
@@ -524,7 +530,8 @@ __device__ __forceinline__ void store_lines(const GemmArgs &p, const Tile &t, co
 #pragma unroll 4
     for (int j = 0; j < BM / kTokens; ++j) {
         const int tok = kTokens * j + (64 * wave + lane) / kPieces, c = lane & (kPieces - 1);
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(buf + (tok * kPieces + (c ^ (tok & 15))) * 16);
+        u32x4 v = *reinterpret_cast<const u32x4 *>(buf + (tok * kPieces + (c ^ (tok & 15))) * 16);
+        if (tok & 16) v = u32x4{v[2], v[3], v[0], v[1]};
         const int64_t n = t.n0 + 8 * c;
         if (tok >= t.rows || n >= p.N) continue;
         uint16_t *dst = p.y + (t.m0 + tok) * p.N + n;
@@ -697,15 +704,16 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
     const int kb_in = min((int)((K - chunk + kBlock - 1) / kBlock - kb0), nkb);
     const uint32_t wlds = lds_address(lds) + wave * 1024, xlds = wlds + C::kXOff;
     const uint32_t slds = lds_address(xsl) + wave * C::kScaleLoads * 256;
-    // Entry (row, block) of a batch of scales at row * kSB + block; entries past
-    // the last block are the next row's, or zero: unused.
+    // Entry (row, block) of a batch of scales at row * kSB + scale_slot(block, row);
+    // entries past the last block are the next row's, or zero: unused.
     auto fill_scales = [&](int kb) __attribute__((always_inline)) {
         const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
         const int f = wave * C::kScaleLoads * 64 + lane;
-        const uint32_t so = (uint32_t)(((f / C::kSB) * p.KB + kb0 + (f & (C::kSB - 1))) * 4);
+        const int row = f / C::kSB, slot = f & (C::kSB - 1);
 #pragma unroll
         for (int j = 0; j < C::kScaleLoads; ++j)
-            fill4(sr, dst + j * 256, so, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
+            fill4(sr, dst + j * 256, (uint32_t)((row * p.KB + kb0 + scale_slot(slot, row + 8 * j)) * 4),
+                  (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
     };
     i32x4 held[ODD ? C::kLoads : 1];   // ODD: the wave's pieces of the block that is next to be stored
     auto take = [&](int kb) __attribute__((always_inline)) {
@@ -798,7 +806,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
                 xf[set][b][s] = *reinterpret_cast<const i32x4 *>(lds + xfrag[s] + (st * C::kStageBytes + b * 4096));
 #pragma unroll
         for (int b = 0; b < SB; ++b)
-            xsv[set][b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+            xsv[set][b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + scale_slot(kb & (C::kSB - 1), rr)];
         wsv[set] = ws_cur;
         ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
     };
@@ -1002,15 +1010,16 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
     auto fill_x = [&](const int st, const int j, int kb) __attribute__((always_inline)) {
         fill16(xr, xlds + st * kStage + j * 8192, xv, j * xstride + (uint32_t)kb * kBlock);
     };
-    // Entry (row, block) of a batch at row * kSB + block; entries past the last
-    // block are the next row's, or zero: unused.
+    // Entry (row, block) of a batch at row * kSB + scale_slot(block, row); entries
+    // past the last block are the next row's, or zero: unused.
     auto fill_scales = [&](int kb) __attribute__((always_inline)) {
         const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
         const int f = wave * C::kScaleLoads * 64 + lane;
-        const uint32_t off = (uint32_t)(((f / C::kSB) * p.KB + (f & (C::kSB - 1))) * 4);
+        const int row = f / C::kSB, slot = f & (C::kSB - 1);
 #pragma unroll
         for (int j = 0; j < C::kScaleLoads; ++j)
-            fill4(sr, dst + j * 256, off, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
+            fill4(sr, dst + j * 256, (uint32_t)((row * p.KB + scale_slot(slot, row + 8 * j)) * 4),
+                  (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
     };
 
     const int rr = lane & 31, hi = lane >> 5;
@@ -1076,7 +1085,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
             read_x(xf[2], st, 1);
 #pragma unroll
             for (int b = 0; b < SB; ++b)
-                xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+                xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + scale_slot(kb & (C::kSB - 1), rr)];
             wsv = ws_cur;
             ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
             if (((kb + 2) & (C::kSB - 1)) == 0) fill_scales(kb + 2);
@@ -1246,15 +1255,16 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     auto fill_x = [&](const int st, const int j, int kb) __attribute__((always_inline)) {
         fill16(xr, xlds + st * kStage + j * 8192, xv, 2 * j * rows32 + (uint32_t)kb * kBlock);
     };
-    // Entry (row, block) of a batch at row * kSB + block; entries past the last
-    // block are the next row's, or zero: unused.
+    // Entry (row, block) of a batch at row * kSB + scale_slot(block, row); entries
+    // past the last block are the next row's, or zero: unused.
     auto fill_scales = [&](int kb) __attribute__((always_inline)) {
         const uint32_t dst = slds + ((kb / C::kSB) & 1) * (C::kBM * C::kSB * 4);
         const int f = wave * C::kScaleLoads * 64 + lane;
-        const uint32_t off = (uint32_t)(((f / C::kSB) * p.KB + (f & (C::kSB - 1))) * 4);
+        const int row = f / C::kSB, slot = f & (C::kSB - 1);
 #pragma unroll
         for (int j = 0; j < C::kScaleLoads; ++j)
-            fill4(sr, dst + j * 256, off, (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
+            fill4(sr, dst + j * 256, (uint32_t)((row * p.KB + scale_slot(slot, row + 8 * j)) * 4),
+                  (uint32_t)(kb * 4 + j * 8 * 4 * (int)p.KB));
     };
 
     const int rr = lane & 31, hi = lane >> 5;
@@ -1320,7 +1330,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
             read_x(xf[2], st, 1);
 #pragma unroll
             for (int b = 0; b < SB; ++b)
-                xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + (kb & (C::kSB - 1))];
+                xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + scale_slot(kb & (C::kSB - 1), rr)];
             wsv = ws_cur;
             ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
             if (((kb + 2) & (C::kSB - 1)) == 0) fill_scales(kb + 2);
