@@ -29,6 +29,14 @@ def _elsewhere(t, name: str, dev: int):
 
 def rows(t, name: str, dev: int, dtype: torch.dtype = torch.bfloat16):
     """Check a 2-D tensor whose rows are contiguous and may lie further apart: (rows, columns, leading dimension)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            shape = t.shape
+            if len(shape) == 2:
+                M, K = shape
+                return M, K, K
+    except AttributeError:
+        pass
     if not isinstance(t, _Tensor) or t.dim() != 2 or t.dtype is not dtype:
         raise TypeError("%s must be a 2-D %s tensor" % (name, str(dtype).replace("torch.", "")))
     if t.get_device() != dev:
@@ -44,8 +52,26 @@ def rows(t, name: str, dev: int, dtype: torch.dtype = torch.bfloat16):
     return M, K, ld
 
 
+def rows_like(t, name: str, dev: int, shape) -> int:
+    """``rows`` of a bf16 tensor of the given shape: its leading dimension."""
+    try:
+        if t.shape == shape and t.dtype is torch.bfloat16 and t.get_device() == dev and t.is_contiguous():
+            return shape[1]
+    except AttributeError:
+        pass
+    M, K, ld = rows(t, name, dev)
+    if (M, K) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), (M, K)))
+    return ld
+
+
 def dense(t, name: str, dev: int, dtype: torch.dtype, shape: tuple):
     """Check a contiguous tensor of the given type and shape (None: any size on that axis)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype is not dtype:
@@ -58,6 +84,18 @@ def dense(t, name: str, dev: int, dtype: torch.dtype, shape: tuple):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t
+
+
+def matrix(t, name: str, dev: int, dtype: torch.dtype, columns: int | None = None):
+    """Check a contiguous 2-D tensor of the given type (and columns): its shape."""
+    try:
+        shape = t.shape
+        if (t.dtype is dtype and len(shape) == 2 and (columns is None or shape[1] == columns)
+                and t.get_device() == dev and t.is_contiguous()):
+            return shape
+    except AttributeError:
+        pass
+    return dense(t, name, dev, dtype, (None, columns)).shape
 
 
 def output(t, name: str, dev: int, dtype: torch.dtype, shape: tuple):

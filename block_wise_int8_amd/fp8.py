@@ -78,8 +78,7 @@ def silu_mul_quant_fp8(h: torch.Tensor, aq: torch.Tensor | None = None, as_: tor
                        return_a: bool = False):
     """h = [gate | up] bf16 [R, 2I] -> (aq float8_e4m3fn [R, I], as float32 [R, ceil(I/128)][, a bf16 [R, I]])."""
     dev = c.device_of(h, "h")
-    c.dense(h, "h", dev, torch.bfloat16, (None, None))
-    R, two_i = h.shape
+    R, two_i = c.matrix(h, "h", dev, torch.bfloat16)
     if two_i % 2:
         raise ValueError("h must have an even number of columns (gate | up)")
     I = two_i // 2
@@ -118,10 +117,8 @@ def gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tens
     ``variant`` (one of ``GEMM_*``) runs a named kernel instead of the
     shape-based choice."""
     dev = c.device_of(xq, "xq")
-    c.dense(xq, "xq", dev, FP8, (None, None))
-    M, K = xq.shape
-    c.dense(w, "w", dev, FP8, (None, K))
-    N = w.shape[0]
+    M, K = c.matrix(xq, "xq", dev, FP8)
+    N, _ = c.matrix(w, "w", dev, FP8, K)
     c.dense(xs, "xs", dev, torch.float32, (M, _blocks(K)))
     c.dense(ws, "ws", dev, torch.float32, (_blocks(N), _blocks(K)))
     if bias is not None:
@@ -142,8 +139,7 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, bias: torch.T
     C call.  ``workspace`` as for gemm_fp8."""
     dev = c.device_of(x, "x")
     M, K, ldx = c.rows(x, "x", dev)
-    c.dense(w, "w", dev, FP8, (None, K))
-    N = w.shape[0]
+    N, _ = c.matrix(w, "w", dev, FP8, K)
     KB = _blocks(K)
     c.dense(ws, "ws", dev, torch.float32, (_blocks(N), KB))
     if bias is not None:
@@ -182,8 +178,7 @@ def moe_gemm_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: torch.Tenso
     ceil(N/128), ceil(K/128)].  ``workspace`` and ``variant`` as for gemm_fp8,
     with ``moe_gemm_fp8_workspace_size`` bytes."""
     dev = c.device_of(xq, "xq")
-    c.dense(xq, "xq", dev, FP8, (None, None))
-    R, K = xq.shape
+    R, K = c.matrix(xq, "xq", dev, FP8)
     c.dense(w, "w", dev, FP8, (None, None, K))
     E, N, _ = w.shape
     c.dense(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
@@ -205,8 +200,7 @@ def moe_gemm_silu_quant_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: 
     up to the order of the products' sums.  w13 is float8_e4m3fn [E, 2I, K]
     (gate rows, then up rows); I % 128 == 0."""
     dev = c.device_of(xq, "xq")
-    c.dense(xq, "xq", dev, FP8, (None, None))
-    R, K = xq.shape
+    R, K = c.matrix(xq, "xq", dev, FP8)
     c.dense(w13, "w13", dev, FP8, (None, None, K))
     E, N, _ = w13.shape
     if N % 2:
@@ -242,8 +236,9 @@ def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13
     given); calls that share one must not overlap in time.  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
     T, H, ldx = c.rows(x, "x", dev)
-    c.dense(logits, "logits", dev, torch.float32, (T, None))
-    E = logits.shape[1]
+    rows, E = c.matrix(logits, "logits", dev, torch.float32)
+    if rows != T:
+        raise ValueError("logits must have %d rows (got %d)" % (T, rows))
     c.dense(w13, "w13", dev, FP8, (E, None, H))
     N = w13.shape[1]
     if N % 2:

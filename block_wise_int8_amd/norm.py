@@ -40,14 +40,12 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, resi
         raise TypeError("the codes are torch.int8 or torch.float8_e4m3fn (got %s)" % dtype)
     ldr = ldh = H
     if residual is not None:
-        rM, rH, ldr = c.rows(residual, "residual", dev)
-        if (rM, rH) != (M, H):
-            raise ValueError("residual must have shape (%d, %d) (got %s)" % (M, H, tuple(residual.shape)))
+        shape = x.shape
+        ldr = c.rows_like(residual, "residual", dev, shape)
         if h is None:
             h = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
-        hM, hH, ldh = c.rows(h, "h", dev)
-        if (hM, hH) != (M, H):
-            raise ValueError("h must have shape (%d, %d) (got %s)" % (M, H, tuple(h.shape)))
+        else:
+            ldh = c.rows_like(h, "h", dev, shape)
     elif h is not None:
         raise ValueError("h is the sum with a residual: there is none")
     xq = c.output(xq, "xq", dev, dtype, (M, H))

@@ -572,3 +572,49 @@ def test_binding_refusals():
     assert torch.equal(layer(), torch.zeros_like(x)) and layer(x=x[:0], logits=logits[:0]).shape == (0, 256)
     assert bi8.gemm_fp8(xq[:0], s[:0], w, ws).shape == (0, 8)
     assert bi8.quant_act_fp8(x[:0])[0].shape == (0, 256)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: their last rows equal the call on those rows alone, bit for bit."""
+    dev = device()
+
+    def same(a, b):
+        assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
+
+    M, H, n = 530000, 4160, 70
+    x = torch.randn(M, H, dtype=torch.bfloat16, device=dev)
+    gain, r = torch.randn(H, dtype=torch.bfloat16, device=dev), torch.randn(n, H, dtype=torch.bfloat16, device=dev)
+    order = torch.arange(M - n, M, dtype=torch.int32, device=dev)
+    for got, want in zip(bi8.quant_act_fp8(x), bi8.quant_act_fp8(x[-n:])):
+        same(got[-n:], want)
+    for got, want in zip(bi8.quant_act_gather_fp8(x, order), bi8.quant_act_fp8(x[-n:])):
+        same(got, want)
+    for dtype in (torch.int8, F8):
+        want = bi8.rmsnorm_quant(x[-n:], gain, residual=x[-n:], dtype=dtype, return_y=True)
+        for got, w in zip(bi8.rmsnorm_quant(x, gain, residual=x, dtype=dtype, return_y=True), want):
+            same(got[-n:], w)
+    h = x.view(-1)[: 76000 * 28672].view(76000, 28672)
+    for got, want in zip(bi8.silu_mul_quant_fp8(h, return_a=True), bi8.silu_mul_quant_fp8(h[-n:], return_a=True)):
+        same(got[-n:], want)
+    del x, h
+    M, N, K = 262300, 8200, 128
+    xq, w = torch.randint(0, 120, (M, K), dtype=torch.uint8, device=dev).view(F8), \
+        torch.randint(0, 120, (N, K), dtype=torch.uint8, device=dev).view(F8)
+    xs, ws = torch.rand(M, 1, device=dev), torch.rand(65, 1, device=dev)
+    for v in VARIANTS:
+        if v == bi8.GEMM_SKINNY:
+            continue
+        same(bi8.gemm_fp8(xq, xs, w, ws, variant=v)[-n:], bi8.gemm_fp8(xq[-n:], xs[-n:], w, ws, variant=v))
+    del xq, xs, w, ws
+    E, N, K = 3, 65536, 16400
+    w = torch.randint(0, 120, (E, N, K), dtype=torch.uint8, device=dev).view(F8)
+    ws = torch.rand(E, N // 128, 129, device=dev)
+    for rows in (2, 70, 300):
+        xq, xs = torch.randint(0, 120, (rows, K), dtype=torch.uint8, device=dev).view(F8), torch.rand(rows, 129, device=dev)
+        off = torch.tensor([0, 0, 0, rows], dtype=torch.int32, device=dev)
+        for v in VARIANTS:
+            same(bi8.moe_gemm_fp8(xq, xs, off, w, ws, variant=v), bi8.gemm_fp8(xq, xs, w[2], ws[2], variant=v))
+        got = bi8.moe_gemm_silu_quant_fp8(xq, xs, off, w, ws)
+        want = bi8.silu_mul_quant_fp8(bi8.gemm_fp8(xq, xs, w[2], ws[2], variant=bi8.GEMM_TILE_256X128))
+        same(got[0], want[0])
+        same(got[1], want[1])
