@@ -736,7 +736,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_tiled_kernel(GemmArgs p)
         }
     };
     auto fill = [&](const int st, int kb) __attribute__((always_inline)) {
-        if ((kb & (C::kSB - 1)) == 0) fill_scales(kb);
+        if (__builtin_expect((kb & (C::kSB - 1)) == 0, 0)) fill_scales(kb);
         if constexpr (ODD) {
             keep(st);
             take(kb + 1);
@@ -1088,7 +1088,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong_kernel(GemmArgs p) {
                 xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + scale_slot(kb & (C::kSB - 1), rr)];
             wsv = ws_cur;
             ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
-            if (((kb + 2) & (C::kSB - 1)) == 0) fill_scales(kb + 2);
+            if (__builtin_expect(((kb + 2) & (C::kSB - 1)) == 0, 0)) fill_scales(kb + 2);
             fill_w(st ^ 1, 2, kb + 1);
             fill_w(st ^ 1, 3, kb + 1);
         } else if constexpr (a == 1) {
@@ -1333,7 +1333,7 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
                 xsv[b] = xsl[(kb / C::kSB) & 1][srow + b * 32 * C::kSB + scale_slot(kb & (C::kSB - 1), rr)];
             wsv = ws_cur;
             ws_cur = ws_row[kb + 1 < nkb ? kb + 1 : nkb - 1];
-            if (((kb + 2) & (C::kSB - 1)) == 0) fill_scales(kb + 2);
+            if (__builtin_expect(((kb + 2) & (C::kSB - 1)) == 0, 0)) fill_scales(kb + 2);
             aim(kb + 2);
             fill_x(after, 0, kb + 2);
             fill_x(after, 1, kb + 2);
