@@ -338,6 +338,21 @@ def test_split_of_a_partial_round():
     assert np.array_equal(bf16_bits(y), fp8.f32_to_bf16(ref.astype(np.float32)))
 
 
+@pytest.mark.parametrize("E,rows", [(40, {3: 1, 39: 2}), (130, {0: 1, 63: 1, 64: 3, 129: 1}), (9, {8: 8}), (70, {})])
+def test_moe_gemm_fewer_rows_than_experts(E, rows):
+    """A decoding step with many experts: a row or two each for a few of them, the last 64 and those around 64
+    among them; R rows of which the segments cover some."""
+    c = grouped_case((78, E), [rows.get(e, 0) for e in range(E)] + [1], 200, 272)
+    xq, xs, off, w, ws = c[0], c[1], c[2][:-1], c[3][:E], c[4][:E]
+    n = sum(rows.values())
+    ref = fp8.moe_gemm_f64(*c)
+    for variant in (None, *VARIANTS):
+        y = torch.full((n + 1, 200), 5.0, dtype=torch.bfloat16, device=device())
+        run_grouped(xq, xs, off, w, ws, y=y, variant=variant)
+        check_product(y[:n], *(r[:n] for r in ref), 272)
+        assert torch.all(y[n:] == 5.0)
+
+
 def test_moe_gemm_rows_past_the_last_segment_stay():
     """Offsets that end before R (a padded batch) leave the rows behind them as they were; offsets outside
     [0, R] are clamped."""
