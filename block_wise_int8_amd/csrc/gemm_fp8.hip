@@ -47,9 +47,11 @@ __device__ __forceinline__ i32x8 join16(i32x4 a, i32x4 b) {
 // load of U blocks is issued before the first MFMA, and the parts' sums meet
 // in LDS.
 //
-// Measured (weights from HBM): 1 x 131072 x 4096 102 us, 5.3 TB/s; 8 x 4096 x
-// 4096 7.3 us, most of it one workgroup's latency; grouped, 16 rows over 8
-// experts of 28672 x 4096 (940 MB, read once by the counters) 137 to 149 us.
+// Measured (weights from HBM): 1 x 131072 x 4096 91 us, 5.9 TB/s; 1 x 4096 x
+// 4096 6.4 us, most of it one workgroup's latency; grouped, 16 rows over 8
+// experts of 28672 x 4096 (940 MB, read once by the counters) 142 us.
+// With 16 tokens or fewer two workgroups share a CU (128 registers at most: at
+// 132, one a CU, 1 x 131072 x 4096 took 152 us).
 //
 // Rows [a, b) of the activations share the weight; they are taken 16 MT at a
 // time.  Dense: [0, M), chunks over blockIdx.y.  MOE: one expert's segment, all
@@ -89,11 +91,12 @@ __device__ __forceinline__ bool expert_with_rows(const GemmArgs &p, uint32_t &e,
 }
 
 template <int MT, bool ODD, bool MOE>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(GemmArgs p, int32_t blocks_per_wave,
-                                                                                   int32_t parts) {
+__global__ __launch_bounds__(kSkinnyWaves * 64)
+    __attribute__((amdgpu_waves_per_eu(MT == 1 && !ODD ? 4 : 2))) void gemm_fp8_skinny_kernel(
+        GemmArgs p, int32_t blocks_per_wave, int32_t parts) {
     constexpr int U = MT <= 3 ? kSkinnyUnroll : 2;
     constexpr int kRows = 16 * MT;
-    __shared__ float red[kSkinnyWaves][MT][64][4];
+    __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][MT][64][4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = kSkinnyWaves / parts;   // weight tiles of this workgroup
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
     const int bp0 = ((lane & 7) * 8 + 2 * quad) * 4;
     const bool upper = row >= 8;
 
-    for (int64_t m0 = a + (int64_t)blockIdx.y * kRows; m0 < b; m0 += (int64_t)gridDim.y * kRows) {
+    auto chunk = [&](int64_t m0) __attribute__((always_inline)) {
         const int mrows = b - m0 < kRows ? (int)(b - m0) : kRows;
         uint32_t xd = 0;
         const __amdgpu_buffer_rsrc_t xr = ODD ? make_rsrc_any(p.xq + m0 * p.K, mrows * K, xd)
@@ -225,24 +228,40 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(Gemm
             }
         }
 
-        // 16x16 result: lane -> token lane & 15, weight rows 4 (lane >> 4) + i
+        // 16x16 result: lane -> token lane & 15, weight rows 4 (lane >> 4) + i.  A
+        // thread adds a lane's four over the parts.
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) red[wave][mt][lane][i] = yv[mt][i];
+        for (int mt = 0; mt < MT; ++mt) *reinterpret_cast<f32x4 *>(red[wave][mt][lane]) = yv[mt];
         __syncthreads();
-        for (int t = threadIdx.x; t < tiles * MT * 256; t += kSkinnyWaves * 64) {
-            const int tile = t / (MT * 256), mt = (t >> 8) % MT, c = (t >> 4) & 15, r = t & 15;
-            const int src = c + 16 * (r >> 2), i = r & 3;
-            float s = 0.f;
-            for (int v = 0; v < parts; ++v) s += red[tile * parts + v][mt][src][i];
-            const int64_t ml = mt * 16 + c, n = wg_n0 + tile * 16 + r;
-            if (ml < mrows && n < p.N) {
-                if (p.bias) s += bf16_bits_to_f32(p.bias[n]);
-                p.y[(m0 + ml) * p.N + n] = (uint16_t)(f32x2_to_bf16x2_bits(s, 0.0f) & 0xFFFFu);
+        for (int t = threadIdx.x; t < tiles * MT * 64; t += kSkinnyWaves * 64) {
+            const int tile = t / (MT * 64), mt = (t >> 6) % MT;
+            f32x4 sum = *reinterpret_cast<const f32x4 *>(red[tile * parts][mt][lane]);
+            for (int v = 1; v < parts; ++v) sum += *reinterpret_cast<const f32x4 *>(red[tile * parts + v][mt][lane]);
+            const int64_t ml = mt * 16 + row, n = wg_n0 + tile * 16 + 4 * quad;
+            if (ml >= mrows || n >= p.N) continue;
+            if (p.bias) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < p.N) sum[i] += bf16_bits_to_f32(p.bias[n + i]);
+            }
+            uint16_t *dst = p.y + (m0 + ml) * p.N + n;
+            const uint2 o = make_uint2(f32x2_to_bf16x2_bits(sum[0], sum[1]), f32x2_to_bf16x2_bits(sum[2], sum[3]));
+            if (p.wide_store) {
+                *reinterpret_cast<uint2 *>(dst) = o;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < p.N) dst[i] = (uint16_t)((i < 2 ? o.x : o.y) >> (16 * (i & 1)));
             }
         }
-        __syncthreads();   // (the next chunk writes the sums again)
+    };
+    if constexpr (!MOE && MT < 4) {   // (all rows are one chunk)
+        chunk(0);
+    } else {
+        for (int64_t m0 = a + (int64_t)blockIdx.y * kRows; m0 < b; m0 += (int64_t)gridDim.y * kRows) {
+            chunk(m0);
+            __syncthreads();   // (the next chunk writes the sums again)
+        }
     }
 }
 
@@ -1480,9 +1499,16 @@ template __global__ void gemm_fp8_pingpong_kernel<false, 4>(GemmArgs);
 template __global__ void gemm_fp8_pingpong_kernel<true, 4>(GemmArgs);
 template __global__ void gemm_fp8_pingpong_kernel<true, 4, true>(GemmArgs);
 
+// Grouped: at least the sum over experts of ceil(rows / bm), of which no more than
+// p.M have rows.
+template <bool MOE>
+int64_t most_tiles_m(const GemmArgs &p, int64_t bm) {
+    return (p.M + bm - 1) / bm + (MOE ? (p.M < p.E ? p.M : p.E) : 0);
+}
+
 template <class C, bool MOE, bool SILU = false>
 hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
-    p.tiles_m = (p.M + C::kBM - 1) / C::kBM + (MOE ? p.E : 0);
+    p.tiles_m = most_tiles_m<MOE>(p, C::kBM);
     p.tiles_n = (p.N + C::kBN - 1) / C::kBN;   // (SILU: I / 128)
     const int64_t total = p.tiles_m * p.tiles_n;
     if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
@@ -1497,8 +1523,7 @@ hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
 
 template <class C, bool MOE, bool SPLIT, int64_t GM, bool ODD = false>
 hipError_t launch_tiled(GemmArgs p, hipStream_t stream, int64_t splits = 1) {
-    // grouped: at least the sum over experts of ceil(rows / BM) tiles
-    p.tiles_m = (p.M + C::kBM - 1) / C::kBM + (MOE ? p.E : 0);
+    p.tiles_m = most_tiles_m<MOE>(p, C::kBM);
     p.tiles_n = (p.N + C::kBN - 1) / C::kBN;
     const int64_t total = p.tiles_m * p.tiles_n + (MOE && SPLIT ? kTailRound : 0);
     if (total > 0x7FFFFFFFll || splits < 1 || splits > 65535) return hipErrorInvalidValue;
