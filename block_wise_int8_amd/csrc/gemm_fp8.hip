@@ -59,6 +59,15 @@ __device__ __forceinline__ i32x8 join16(i32x4 a, i32x4 b) {
 // ODD: K % 16 != 0, rows start at any byte (see buf_load16_any).
 constexpr int kSkinnyWaves = 8;
 constexpr int kSkinnyUnroll = 4;
+constexpr int skinny_unroll(int64_t mt) { return mt <= 3 ? kSkinnyUnroll : 2; }
+
+// Host: 16-token groups of a chunk for so many rows, and waves that share a tile's K.
+int64_t skinny_mt(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 4; }
+int32_t skinny_parts(int64_t KB) {
+    int32_t parts = kSkinnyWaves;
+    while (parts > 1 && KB <= parts / 2 * kSkinnyUnroll) parts /= 2;
+    return parts;
+}
 
 // With fewer rows than experts the grid covers as many experts as there are rows,
 // and e, the number of one among those that have rows, becomes its index, [a, b)
@@ -94,7 +103,7 @@ template <int MT, bool ODD, bool MOE>
 __global__ __launch_bounds__(kSkinnyWaves * 64)
     __attribute__((amdgpu_waves_per_eu(MT == 1 && !ODD ? 4 : 2))) void gemm_fp8_skinny_kernel(
         GemmArgs p, int32_t blocks_per_wave, int32_t parts) {
-    constexpr int U = MT <= 3 ? kSkinnyUnroll : 2;
+    constexpr int U = skinny_unroll(MT);
     constexpr int kRows = 16 * MT;
     __shared__ __attribute__((aligned(16))) float red[kSkinnyWaves][MT][64][4];
     const int lane = threadIdx.x & 63;
@@ -268,8 +277,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64)
 // chunks: workgroups that share the rows of one weight tile (dense)
 template <int MT, bool ODD, bool MOE>
 hipError_t launch_skinny_mt(GemmArgs p, int64_t chunks, hipStream_t stream) {
-    int32_t parts = kSkinnyWaves;
-    while (parts > 1 && p.KB <= parts / 2 * kSkinnyUnroll) parts /= 2;
+    const int32_t parts = skinny_parts(p.KB);
     const int64_t rows = 16 * (kSkinnyWaves / parts);
     p.tiles_n = (p.N + rows - 1) / rows;
     const int64_t blocks = p.tiles_n * (MOE && p.M < p.E ? p.M : p.E);
@@ -284,7 +292,7 @@ hipError_t launch_skinny_mt(GemmArgs p, int64_t chunks, hipStream_t stream) {
 // rows: how many rows a weight tile is likely to meet (dense: M)
 template <bool ODD, bool MOE>
 hipError_t launch_skinny(const GemmArgs &p, int64_t rows, hipStream_t stream) {
-    const int64_t mt = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 4;
+    const int64_t mt = skinny_mt(rows);
     const int64_t chunks = MOE ? 1 : (p.M + 16 * mt - 1) / (16 * mt);
     switch (mt) {
         case 1: return launch_skinny_mt<1, ODD, MOE>(p, chunks, stream);
@@ -1548,22 +1556,25 @@ hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
 // Choice of the kernel
 // ---------------------------------------------------------------------------
 //
-// A tile takes a time per K block that hardly depends on the problem (one
-// workgroup a CU): measured at K = 4096, with few tiles on the chip and with
-// all 256 CUs taken.  The estimate of a launch is its rounds of tiles, the
-// last one's by how full it is; split over K, a unit walks its share of the
-// blocks, and the partial sums are written and read once.  The choice is the
-// smallest estimate.
+// A tile takes a time of its own (first fills, stores) and one per K block, with few
+// tiles on the chip and with all 256 CUs taken (one workgroup a CU).  The estimate
+// of a launch is its rounds of tiles, the last one's by how full it is, and the
+// weight's stream beside them; split over K, a unit walks its share of the blocks,
+// and the partial sums are written and read once.  The choice is the smallest
+// estimate.  The constants are fitted to 700 products of sizes drawn over 1 to 8192
+// rows, 64 to 28672 columns, K 128 to 14336 and up to 64 experts, where the chosen
+// kernel takes 0.3 % (dense) and 0.8 % (grouped) longer than the fastest of the
+// five on average.
 struct Tiling {
     Fp8Path path;
     int bn, bm;
-    double light, full;   // us a K block
+    double light, full, tile;   // us a K block, us a tile
 };
 constexpr Tiling kTilings[] = {
-    {Fp8Path::kTile128x64, 128, 64, 0.42, 0.52},
-    {Fp8Path::kTile128x128, 128, 128, 0.61, 0.75},
-    {Fp8Path::kTile256x128, 256, 128, 0.92, 1.10},
-    {Fp8Path::kTile256x256, 256, 256, 1.25, 1.90},
+    {Fp8Path::kTile128x64, 128, 64, 0.32, 0.56, 3.2},
+    {Fp8Path::kTile128x128, 128, 128, 0.48, 0.73, 3.8},
+    {Fp8Path::kTile256x128, 256, 128, 0.71, 1.27, 4.7},
+    {Fp8Path::kTile256x256, 256, 256, 1.00, 1.60, 5.8},
 };
 constexpr double kCUs = 256;
 constexpr int64_t kMaxPartialBytes = 64ll << 20;
@@ -1576,13 +1587,25 @@ struct Choice {
 
 double tiles_us(const Tiling &t, double tiles, int64_t blocks) {
     const double rounds = (double)(int64_t)(tiles / kCUs), rest = tiles - rounds * kCUs;
-    return blocks * (rounds * t.full + (rest > 0 ? t.light + (t.full - t.light) * rest / kCUs : 0));
+    const double last = rest > 0 ? t.tile + blocks * (t.light + (t.full - t.light) * rest / kCUs) : 0;
+    return rounds * (t.tile + blocks * t.full) + last;
 }
 
 // The launch, the tiles' time and the weight's stream, which overlap, the
 // shorter one not quite.
 double overlapped_us(double tiles, double stream) {
-    return 3 + (tiles < stream ? stream + 0.15 * tiles : tiles + 0.15 * stream);
+    return 1.7 + (tiles < stream ? stream + 0.15 * tiles : tiles + 0.15 * stream);
+}
+
+// The streaming kernel: the weight's stream, longer where a wave's blocks leave
+// loads of its last round unused and with more rows (`more`), and no less than the
+// time of a chunk of so many rows.
+double streaming_us(double stream, double rows, double more, double chunk, int64_t KB) {
+    const int64_t mine = (KB + skinny_parts(KB) - 1) / skinny_parts(KB);
+    const int64_t unroll = skinny_unroll(skinny_mt((int64_t)rows));
+    const double waste = KB > 8 ? (double)((mine + unroll - 1) / unroll * unroll) / mine : 1;
+    const double us = 4 + stream * waste * (1 + more), least = 4.2 + chunk * rows;
+    return us < least ? least : us;
 }
 
 // Rows at any byte have two kernels: the streaming one, its loads made of
@@ -1593,19 +1616,16 @@ bool odd_rows_streamed(int64_t M, int64_t N) { return N * (16 + M) <= 1000000; }
 
 // partial: bytes of fp32 partial sums that may be used (0: no split).
 // The streaming kernel reads the activations again for every 16 weight rows, and
-// for more than 16 tokens a wave has half the weight in flight.  Measured
-// (streaming / 128 x 64, us, weights from HBM, K = 4096): M = 1, N = 131072
-// 102 / 117, M = 8, N = 28672 28.4 / 30.9, M = 16 33.9 / 30.8, M = 32, N = 14336
-// 32.3 / 22.4, M = 64, N = 4096 16.5 / 18.9 (13.1 split over K), M = 64, N = K =
-// 2048 15.4 / 9.8, M = 16, N = 8192, K = 28672 71 / 98 (47 split).
+// for more than 16 tokens a CU holds one workgroup, not two.  Measured (streaming /
+// 128 x 64, us, weights from HBM, K = 4096): M = 1, N = 131072 91 / 117, M = 16, N =
+// 28672 31.2 / 30.8, M = 32, N = 14336 31 / 22.4, M = 64, N = 4096 16.0 / 18.9 (13.1
+// split over K), M = 64, N = K = 2048 15.4 / 9.8, M = 16, N = 8192, K = 28672 71 / 98
+// (47 split).
 Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
     Choice best;
     const double bytes = (double)N * (double)K;
-    if (M <= 64) {
-        best.us = 4 + bytes / 5.5e6 * (1 + (M - 1) * (M <= 16 ? 0.025 : 0.047));
-        if (best.us < 2 + 0.2 * M) best.us = 2 + 0.2 * M;
-    }
     const int64_t KB = (K + kBlock - 1) / kBlock;
+    if (M <= 64) best.us = streaming_us(bytes / 5.5e6, (double)M, (M - 1) * (M <= 16 ? 0.02 : 0.047), 0.2, KB);
     for (const Tiling &t : kTilings) {
         const double tiles = (double)((M + t.bm - 1) / t.bm) * (double)((N + t.bn - 1) / t.bn);
         const bool may_split = t.bn == 128;
@@ -1613,7 +1633,7 @@ Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
             const int64_t per = (KB + z - 1) / z;
             if (z > 1 && (tiles * z > kCUs || per < 4 || z * M * N * 4 > partial || (KB + per - 1) / per != z)) continue;
             const double us = overlapped_us(tiles_us(t, tiles * z, per), bytes / 4.9e6) +
-                              (z > 1 ? 4 + 8e-6 * z * M * N / 4 : 0);
+                              (z > 1 ? 3 + 8e-6 * z * M * N / 4 : 0);
             if (us < best.us) {
                 best.path = t.path;
                 best.splits = z;
@@ -1625,9 +1645,8 @@ Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
 }
 
 // Segments are ragged and only the device knows them: R rows spread evenly over
-// the experts, and half a tile more for each.  Every expert's weight is read,
-// at 5.5 TB/s by the tiled kernels and 6.3 by the streaming one, which takes
-// more time with more rows an expert.
+// the experts, and half a tile more for each.  Every expert's weight is read, at
+// 5.5 TB/s by the tiled kernels and 6.3 by the streaming one.
 struct Grouped {
     double experts, mean, bytes;   // experts with rows, rows of each, bytes of their weights
     int64_t N, KB;
@@ -1644,8 +1663,7 @@ struct Grouped {
 Choice choose_grouped(int64_t R, int64_t N, int64_t K, int32_t E, int64_t partial) {
     const Grouped g(R, N, K, E);
     Choice best;
-    best.us = 3 + g.bytes / 6.35e6 * (1 + (g.mean > 2 ? (g.mean - 2) / 16 : 0));
-    if (best.us < 2 + 0.25 * g.mean) best.us = 2 + 0.25 * g.mean;
+    best.us = streaming_us(g.bytes / 6.35e6, g.mean, g.mean > 2 ? (g.mean - 2) / 12 : 0, 0.25, g.KB);
     for (const Tiling &t : kTilings) {
         const double tiles = g.tiles(t);
         double us = tiles_us(t, tiles, g.KB);

@@ -299,6 +299,7 @@ SEGMENTS = [
     ([40, 0, 0, 65, 1], 256, 384), ([0, 0, 200], 300, 144), ([130, 7, 260, 0, 33], 640, 272),
     ([300, 1, 513], 1030, 256), ([1] * 70, 64, 128), ([9] * 33, 200, 160), ([700, 0, 2], 2050, 1168),
     ([0] * 130 + [5] + [0] * 60 + [150, 3], 130, 144), ([150, 0, 201, 150], 1031, 4112), ([513, 30], 130, 2064),
+    ([150, 0, 201, 150], 519, 8208), ([7, 0, 80], 200, 9232),
 ]
 
 
@@ -325,12 +326,12 @@ def test_moe_every_variant(segments, N, K, variant):
 def test_split_of_a_partial_round():
     """A grouped problem whose tiles are split over K, an exact one: split and whole agree bit for bit."""
     rng = np.random.default_rng(75)
-    segments, N, K = [150, 0, 201, 150], 1031, 4112
+    segments, N, K = [150, 0, 201, 150], 519, 8208
     E, R = len(segments), sum(segments)
     assert bi8.moe_gemm_fp8_workspace_size(R, N, K, E) > 0
     off = np.concatenate([[0], np.cumsum(segments)]).astype(np.int32)
     xq, w = fp8.encode(rng.integers(-3, 4, (R, K))), fp8.encode(rng.integers(-3, 4, (E, N, K)))
-    xs, ws = np.ones((R, 33), np.float32), np.exp2(rng.integers(-2, 1, (E, 9, 33))).astype(np.float32)
+    xs, ws = np.ones((R, 65), np.float32), np.exp2(rng.integers(-2, 1, (E, 5, 65))).astype(np.float32)
     wsp = torch.empty(bi8.moe_gemm_fp8_workspace_size(R, N, K, E), dtype=torch.uint8, device=device())
     y = run_grouped(xq, xs, off, w, ws, workspace=wsp)
     assert torch.equal(y.view(torch.int16), run_grouped(xq, xs, off, w, ws).view(torch.int16))
