@@ -436,7 +436,8 @@ def run_layer(x, logits, w13, s13, w2, s2, k):
 
 
 @pytest.mark.parametrize("T,E,H,I,k", [(1, 2, 128, 128, 1), (3, 8, 256, 144, 2), (40, 3, 384, 256, 2), (257, 5, 256, 400, 4),
-                                       (700, 4, 512, 640, 2), (1200, 3, 640, 1280, 2), (1000, 2, 640, 2048, 2)])
+                                       (700, 4, 512, 640, 2), (1200, 3, 640, 1280, 2), (1000, 2, 640, 2048, 2),
+                                       (9, 130, 256, 128, 8), (2, 1000, 128, 48, 1)])
 def test_moe_layer_stage_by_stage(T, E, H, I, k):
     """Every stage against the oracle fed with the stage's own inputs (a sum rounded to the other neighbour
     moves a code by a whole step, so the end of the chain has no tolerance of its own), and the layer
