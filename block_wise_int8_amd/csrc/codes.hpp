@@ -103,7 +103,10 @@ struct E4m3Codes {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = s == 0.0f ? 0.0f : fminf(fmaxf(f[i] / s, -kMax), kMax);
+            for (int i = 0; i < 8; ++i) {
+                const float v = f[i] / s;   // (NaN stays NaN: infinity over an infinite scale)
+                q[i] = s == 0.0f ? 0.0f : v > kMax ? kMax : v < -kMax ? -kMax : v;
+            }
         }
         int a = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
         a = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], a, true);

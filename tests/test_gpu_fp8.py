@@ -264,7 +264,9 @@ def test_gemm_leaves_what_is_not_its_own():
         check_product(room[1: M * N + 1].view(M, N), *fp8.gemm_f64(*c), K)
 
 
-@pytest.mark.parametrize("M,N,K,pad", [(1, 512, 256, 0), (9, 300, 130, 3), (80, 256, 1040, 8), (400, 700, 384, 0)])
+@pytest.mark.parametrize("M,N,K,pad", [(1, 512, 256, 0), (9, 300, 130, 3), (80, 256, 1040, 8), (400, 700, 384, 0),
+                                       (1, 4096, 4096, 0), (8, 4090, 4096, 8), (16, 256, 1040, 0), (16, 40, 112, 16),
+                                       (3, 5000, 2320, 24), (5, 1000, 16, 0), (16, 130, 9232, 0), (2, 200, 4352, 4)])
 def test_linear_is_the_two_calls(M, N, K, pad):
     rng = wl.rng_for((67, M, N, K))
     x = bf16_to_dev(wl.activations(rng, M, K + pad, 0.01))[:, :K]
@@ -276,6 +278,29 @@ def test_linear_is_the_two_calls(M, N, K, pad):
     assert torch.equal(y.view(torch.int16), bi8.gemm_fp8(xq, xs, wq, ws, b).view(torch.int16))
     assert torch.equal(q2.view(torch.uint8), xq.view(torch.uint8)) and torch.equal(s2, xs)
     check_product(y, *fp8.gemm_f64(codes_host(xq), xs.cpu().numpy(), codes_host(wq), ws.cpu().numpy(), bf16_bits(b)), K)
+
+
+@pytest.mark.parametrize("M", [3, 16, 40])
+def test_linear_zero_and_non_finite_groups(M):
+    """Rows with groups of zeros, tiny values, a NaN and an infinity, as the two calls have them: codes and scales
+    bit for bit where the group is finite, NaN outputs in the rows with a NaN or an infinity only."""
+    N, K = 200, 400
+    rng = wl.rng_for((68, M))
+    x = bf16_to_dev(wl.activations(rng, M, K, 0.01))
+    x[0, :128] = 0.0
+    x[0, 128:256] *= 1e-38
+    x[1, 300], x[2, 5] = float("nan"), float("inf")
+    wq, ws = bi8.quant_weight_fp8(bf16_to_dev(wl.activations(rng, N, K)))
+    xq, xs = bi8.quant_act_fp8(x)
+    q2, s2 = torch.empty_like(xq), torch.empty_like(xs)
+    y = bi8.linear_fp8(x, wq, ws, xq=q2, xs=s2)
+    assert torch.equal(s2.nan_to_num(nan=-1.0), xs.nan_to_num(nan=-1.0))
+    fine = torch.isfinite(xs).repeat_interleave(128, 1)[:, :K]
+    assert torch.equal(q2.view(torch.uint8)[fine], xq.view(torch.uint8)[fine])
+    nan = torch.isnan(y).all(1)
+    assert nan.nonzero().flatten().tolist() == [1, 2] and torch.isfinite(y[~nan]).all()
+    want = bi8.gemm_fp8(xq, xs, wq, ws)
+    assert torch.equal(y[~nan].view(torch.int16), want[~nan].view(torch.int16))
 
 
 # ----------------------------------------------------------------- grouped --
