@@ -130,6 +130,11 @@ def _ptr(t):
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
+    try:
+        if t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
@@ -241,7 +246,7 @@ def gemm_ws(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tenso
     if w.shape[1] != K:
         raise ValueError("w must be [N, K] with K = %d (got %s)" % (K, tuple(w.shape)))
     NB, KB = scale_shape(N, K, *block)
-    if tuple(xs.shape) != (M, KB) or tuple(ws.shape) != (NB, KB):
+    if xs.shape != (M, KB) or ws.shape != (NB, KB):
         raise ValueError("scale shapes must be xs [M, %d] and ws [%d, %d]" % (KB, NB, KB))
     if bias is not None:
         _need(bias, "bias", torch.bfloat16, 1)
@@ -250,13 +255,13 @@ def gemm_ws(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tenso
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
     _need(y, "y", torch.bfloat16, 2)
-    if tuple(y.shape) != (M, N):
+    if y.shape != (M, N):
         raise ValueError("y must be [M, N]")
     nbytes = 0
     if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device.type != "cuda" or not workspace.is_contiguous():
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on a HIP device")
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = workspace.nbytes
     _check(load().blockint8_gemm_ws(_ptr(xq), _ptr(xs), _ptr(w), _ptr(ws), _ptr(bias), _ptr(y), M, N, K,
                                     block[0], block[1], _ptr(workspace), nbytes, _stream_handle(xq.device)))
     return y
