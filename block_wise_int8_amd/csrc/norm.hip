@@ -187,11 +187,25 @@ __global__ __launch_bounds__(256) void rmsnorm_quant_kernel(NormArgs p) {
 }
 
 template <class Codes, int W, int C, bool ODD>
-hipError_t launch(const NormArgs &p, hipStream_t stream) {
-    const int64_t blocks = W == 1 ? (p.M + 3) / 4 : p.M;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((rmsnorm_quant_kernel<Codes, W, C, ODD>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
-    return hipGetLastError();
+hipError_t launch(NormArgs p, hipStream_t stream) {
+    constexpr int64_t kRows = W == 1 ? 4 : 1;   // of a workgroup
+    for (int64_t left = p.M; left > 0;) {
+        p.M = left < kBandWorkgroups * kRows ? left : kBandWorkgroups * kRows;
+        hipLaunchKernelGGL((rmsnorm_quant_kernel<Codes, W, C, ODD>), dim3((unsigned)((p.M + kRows - 1) / kRows)),
+                           dim3(256), 0, stream, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        left -= p.M;
+        p.x += p.M * p.ldx;
+        if (p.residual) {
+            p.residual += p.M * p.ldr;
+            p.h += p.M * p.ldh;
+        }
+        if (p.y) p.y += p.M * p.H;
+        p.xq += p.M * p.H;
+        p.xs += p.M * p.HB;
+    }
+    return hipSuccess;
 }
 
 // four waves a row, by the sweeps of 2048 columns that it takes

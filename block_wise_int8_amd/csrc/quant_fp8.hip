@@ -158,37 +158,47 @@ hipError_t launch_quant_act_fp8(const uint16_t *x, int64_t src_rows, int64_t ldx
     const bool two = M * KB >= 8192;   // enough groups to fill the chip with two per lane
     const int64_t gpw = two ? 8 : 4;           // groups per wave
     const int64_t waves_per_row = (KB + gpw - 1) / gpw;
-    const int64_t total_waves = M * waves_per_row;
-    const int64_t blocks = (total_waves + kQuantWaves - 1) / kQuantWaves;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-    if (blocks == 0) return hipSuccess;
-    const dim3 grid((unsigned)blocks), block(kQuantWaves * 64);
-    if (odd && two)
-        hipLaunchKernelGGL((quant_act_fp8_kernel<2, true>), grid, block, 0, stream, x, K, ldx, xq, xs, KB,
-                           waves_per_row, total_waves, rows, src_rows);
-    else if (odd)
-        hipLaunchKernelGGL((quant_act_fp8_kernel<1, true>), grid, block, 0, stream, x, K, ldx, xq, xs, KB,
-                           waves_per_row, total_waves, rows, src_rows);
-    else if (two)
-        hipLaunchKernelGGL((quant_act_fp8_kernel<2, false>), grid, block, 0, stream, x, K, ldx, xq, xs, KB,
-                           waves_per_row, total_waves, rows, src_rows);
-    else
-        hipLaunchKernelGGL((quant_act_fp8_kernel<1, false>), grid, block, 0, stream, x, K, ldx, xq, xs, KB,
-                           waves_per_row, total_waves, rows, src_rows);
-    return hipGetLastError();
+    const int64_t band = kBandWorkgroups * kQuantWaves / waves_per_row;   // rows a launch (K <= 2^23: 2048 or more)
+    for (int64_t m0 = 0; m0 < M; m0 += band) {
+        const int64_t total_waves = (M - m0 < band ? M - m0 : band) * waves_per_row;
+        const dim3 grid((unsigned)((total_waves + kQuantWaves - 1) / kQuantWaves)), block(kQuantWaves * 64);
+        const uint16_t *src = rows ? x : x + m0 * ldx;
+        const int32_t *idx = rows ? rows + m0 : nullptr;
+        const int64_t nsrc = rows ? src_rows : src_rows - m0;
+        uint8_t *q = xq + m0 * K;
+        float *s = xs + m0 * KB;
+        if (odd && two)
+            hipLaunchKernelGGL((quant_act_fp8_kernel<2, true>), grid, block, 0, stream, src, K, ldx, q, s, KB,
+                               waves_per_row, total_waves, idx, nsrc);
+        else if (odd)
+            hipLaunchKernelGGL((quant_act_fp8_kernel<1, true>), grid, block, 0, stream, src, K, ldx, q, s, KB,
+                               waves_per_row, total_waves, idx, nsrc);
+        else if (two)
+            hipLaunchKernelGGL((quant_act_fp8_kernel<2, false>), grid, block, 0, stream, src, K, ldx, q, s, KB,
+                               waves_per_row, total_waves, idx, nsrc);
+        else
+            hipLaunchKernelGGL((quant_act_fp8_kernel<1, false>), grid, block, 0, stream, src, K, ldx, q, s, KB,
+                               waves_per_row, total_waves, idx, nsrc);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_silu_mul_quant_fp8(const uint16_t *h, int64_t R, int64_t I, uint8_t *aq, float *as,
                                      uint16_t *a_out, hipStream_t stream) {
     const int64_t IB = (I + kBlock - 1) / kBlock;
     const int64_t waves_per_row = (IB + 4 * kGateChunks - 1) / (4 * kGateChunks);
-    const int64_t total_waves = R * waves_per_row;
-    const int64_t blocks = (total_waves + kQuantWaves - 1) / kQuantWaves;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-    if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(silu_mul_quant_fp8_kernel, dim3((unsigned)blocks), dim3(kQuantWaves * 64), 0, stream, h, I, aq,
-                       as, a_out, IB, waves_per_row, total_waves);
-    return hipGetLastError();
+    const int64_t band = kBandWorkgroups * kQuantWaves / waves_per_row;
+    for (int64_t r0 = 0; r0 < R; r0 += band) {
+        const int64_t total_waves = (R - r0 < band ? R - r0 : band) * waves_per_row;
+        hipLaunchKernelGGL(silu_mul_quant_fp8_kernel, dim3((unsigned)((total_waves + kQuantWaves - 1) / kQuantWaves)),
+                           dim3(kQuantWaves * 64), 0, stream, h + r0 * 2 * I, I, aq + r0 * I, as + r0 * IB,
+                           a_out ? a_out + r0 * I : nullptr, IB, waves_per_row, total_waves);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_quant_weight_fp8(const uint16_t *w, int64_t N, int64_t K, int64_t ldw, uint8_t *wq, float *ws,
