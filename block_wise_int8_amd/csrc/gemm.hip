@@ -1407,7 +1407,7 @@ template <bool PC, bool ODD>
 hipError_t launch_skinny(GemmArgs p, hipStream_t stream) {
     const int64_t tiles = (p.N + 15) / 16;
     const int64_t chunks = ODD ? (p.M + kSkinnyMaxM - 1) / kSkinnyMaxM : 1;
-    if (tiles > 0x7FFFFFFFll || chunks > 65535) return hipErrorInvalidValue;
+    if (!launch_fits(tiles, kSkinnyWaves * 64) || chunks > 65535) return hipErrorInvalidValue;
     if (tiles == 0 || chunks == 0) return hipSuccess;
     const int32_t bpw = (int32_t)((p.KB + kSkinnyWaves - 1) / kSkinnyWaves);
     const dim3 grid((unsigned)tiles, (unsigned)chunks), block(kSkinnyWaves * 64);
@@ -1427,7 +1427,7 @@ hipError_t launch_tiled(GemmArgs p, hipStream_t stream, int32_t splits = 1) {
     using C = TileCfg<WN, WM, SA, SB>;
     const int64_t total = p.tiles_m * p.tiles_n;
     if (total <= 0) return hipSuccess;
-    if (total > 0x7FFFFFFFll || splits < 1 || splits > 65535) return hipErrorInvalidValue;
+    if (!launch_fits(total, C::kThreads) || splits < 1 || splits > 65535) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_tiled_kernel<WN, WM, SA, SB, MOE, PING, NS, SPLIT>),
                        dim3((unsigned)total, (unsigned)splits), dim3(C::kThreads), 0, stream, p);
     return hipGetLastError();
@@ -1437,7 +1437,7 @@ template <bool MOE, bool SILU = false>
 hipError_t launch_wide(GemmArgs p, hipStream_t stream) {
     const int64_t total = p.tiles_m * p.tiles_n;
     if (total <= 0) return hipSuccess;
-    if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(total, WideCfg::kThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_wide_kernel<MOE, SILU>), dim3((unsigned)total), dim3(WideCfg::kThreads), 0,
                        stream, p);
     return hipGetLastError();
@@ -1559,7 +1559,7 @@ hipError_t launch_gemm_ws(const int8_t *xq, const float *xs, const int8_t *w, co
     const bool vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
     const int64_t threads = vec ? (M * N) / 4 : M * N;
     const int64_t blocks = (threads + 255) / 256;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
     if (vec)
         hipLaunchKernelGGL(splitk_reduce_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, workspace, splits,
                            M, N, bias, y);
@@ -1581,7 +1581,7 @@ hipError_t launch_gemm_per_channel(const int8_t *xq, const float *xs, const int8
         p.tiles_m = (M + 255) / 256;
         p.tiles_n = (N + 255) / 256;
         const int64_t total = p.tiles_m * p.tiles_n;
-        if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
+        if (!launch_fits(total, WideCfg::kThreads)) return hipErrorInvalidValue;
         hipLaunchKernelGGL(gemm_perch_wide_kernel, dim3((unsigned)total), dim3(WideCfg::kThreads), 0, stream, p);
         return hipGetLastError();
     }
@@ -1589,7 +1589,7 @@ hipError_t launch_gemm_per_channel(const int8_t *xq, const float *xs, const int8
     p.tiles_n = (N + 255) / 256;
     const int64_t total = p.tiles_m * p.tiles_n;
     if (total <= 0) return hipSuccess;
-    if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(total, 512)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_perch_kernel<false>), dim3((unsigned)total), dim3(512), 0, stream, p);
     return hipGetLastError();
 }
@@ -1634,7 +1634,7 @@ hipError_t launch_moe_gemm_ws(const int8_t *xq, const float *xs, const int32_t *
     p.tiles_n = (N + 255) / 256;
     // every tile of that bound, plus one round for the split units
     const int64_t grid = p.tiles_m * p.tiles_n + kTailRound;
-    if (grid > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(grid, 512)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_tiled_kernel<4, 2, 2, 2, true, true, 3, true>), dim3((unsigned)grid), dim3(512), 0,
                        stream, p);
     hipError_t e = hipGetLastError();

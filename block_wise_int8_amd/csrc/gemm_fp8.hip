@@ -281,7 +281,7 @@ hipError_t launch_skinny_mt(GemmArgs p, int64_t chunks, hipStream_t stream) {
     const int64_t rows = 16 * (kSkinnyWaves / parts);
     p.tiles_n = (p.N + rows - 1) / rows;
     const int64_t blocks = p.tiles_n * (MOE && p.M < p.E ? p.M : p.E);
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, kSkinnyWaves * 64)) return hipErrorInvalidValue;
     if (chunks > 65535) chunks = 65535;
     const int32_t bpw = (int32_t)((p.KB + parts - 1) / parts);
     hipLaunchKernelGGL((gemm_fp8_skinny_kernel<MT, ODD, MOE>), dim3((unsigned)blocks, (unsigned)chunks),
@@ -1519,7 +1519,7 @@ hipError_t launch_pingpong(GemmArgs p, hipStream_t stream) {
     p.tiles_m = most_tiles_m<MOE>(p, C::kBM);
     p.tiles_n = (p.N + C::kBN - 1) / C::kBN;   // (SILU: I / 128)
     const int64_t total = p.tiles_m * p.tiles_n;
-    if (total > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(total, C::kThreads)) return hipErrorInvalidValue;
     if constexpr (C::kBM == 256)
         hipLaunchKernelGGL((gemm_fp8_pingpong_kernel<MOE, 4, SILU>), dim3((unsigned)total), dim3(C::kThreads), 0, stream,
                            p);
@@ -1534,7 +1534,7 @@ hipError_t launch_tiled(GemmArgs p, hipStream_t stream, int64_t splits = 1) {
     p.tiles_m = most_tiles_m<MOE>(p, C::kBM);
     p.tiles_n = (p.N + C::kBN - 1) / C::kBN;
     const int64_t total = p.tiles_m * p.tiles_n + (MOE && SPLIT ? kTailRound : 0);
-    if (total > 0x7FFFFFFFll || splits < 1 || splits > 65535) return hipErrorInvalidValue;
+    if (!launch_fits(total, C::kThreads) || splits < 1 || splits > 65535) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_fp8_tiled_kernel<C, MOE, SPLIT, GM, ODD>), dim3((unsigned)total, (unsigned)splits),
                        dim3(C::kThreads), 0, stream, p);
     return hipGetLastError();
@@ -1730,7 +1730,7 @@ hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, con
     if (e != hipSuccess) return e;
     const bool vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
     const int64_t blocks = ((vec ? M * N / 4 : M * N) + 255) / 256;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
     if (vec)
         hipLaunchKernelGGL(splitk_reduce_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, workspace,
                            c.splits, M, N, bias, y);

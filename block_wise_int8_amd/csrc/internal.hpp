@@ -8,9 +8,13 @@
 namespace bi8 {
 
 // A launch counts its threads along a dimension in 32 bits: one of 2^32 or more
-// reports no error and runs the remainder modulo 2^32.  Row-wise kernels therefore
-// take their rows in bands of at most this many workgroups (2^23 of 256 threads).
+// reports no error and runs the remainder modulo 2^32.
+constexpr bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups * threads <= 0xFFFFFFFFll; }
+
+// Row-wise kernels of the e4m3 layer and the norm take their rows in bands of at
+// most so many workgroups of 256 threads.
 constexpr int64_t kBandWorkgroups = 1ll << 23;
+static_assert(launch_fits(kBandWorkgroups, 256), "a band is one launch");
 
 // GEMM kernels (the values are the BI8_GEMM_* variant ids of the C ABI).
 enum class GemmPath : int { kAuto = 0, kSkinny = 1, kTile128x64 = 2, kTile256x128 = 3, kTile256x256 = 4 };

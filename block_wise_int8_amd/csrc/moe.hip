@@ -308,7 +308,7 @@ hipError_t launch_moe_route(const float *logits, int64_t T, int32_t E, int32_t k
     if (E > kMaxExperts || k > 8) return hipErrorInvalidValue;
     if (T > 0) {
         const int64_t blocks = (T + 255) / 256;
-        if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+        if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
         if (E <= 16)
             hipLaunchKernelGGL(moe_topk_kernel<16>, dim3((unsigned)blocks), dim3(256), 0, stream, logits, T, E, k,
                                renorm, ids, weights);
@@ -345,7 +345,7 @@ hipError_t launch_silu_mul_quant(const uint16_t *h, int64_t R, int64_t I, int8_t
     const int64_t waves_per_row = (IB + 4 * kSiluChunks - 1) / (4 * kSiluChunks);
     const int64_t total_waves = R * waves_per_row;
     const int64_t blocks = (total_waves + kSiluWaves - 1) / kSiluWaves;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, kSiluWaves * 64)) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(silu_mul_quant_kernel, dim3((unsigned)blocks), dim3(kSiluWaves * 64), 0, stream, h, I,
                        aq, as, a_out, IB, waves_per_row, total_waves);
@@ -356,7 +356,7 @@ hipError_t launch_moe_combine(const uint16_t *y2, int64_t R, const int32_t *row_
                               int64_t T, int32_t k, int64_t H, uint16_t *out, hipStream_t stream) {
     const int64_t threads = T * (H / 8);
     const int64_t blocks = (threads + 255) / 256;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, 256)) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, y2, R, row_of, w, T, k,
                        H, out);

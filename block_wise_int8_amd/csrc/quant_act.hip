@@ -90,7 +90,7 @@ hipError_t launch_quant_act_gather(const uint16_t *x, int64_t src_rows, int64_t 
     const int64_t waves_per_row = (KB + gpw - 1) / gpw;
     const int64_t total_waves = M * waves_per_row;
     const int64_t blocks = (total_waves + kQuantWaves - 1) / kQuantWaves;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, kQuantWaves * 64)) return hipErrorInvalidValue;
     if (blocks == 0) return hipSuccess;
     const dim3 grid((unsigned)blocks), block(kQuantWaves * 64);
     if (odd)
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(256) void quant_act_token_kernel(const uint16_t *__
 hipError_t launch_quant_act_per_token(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, int8_t *xq,
                                       float *xs, hipStream_t stream) {
     if (M == 0) return hipSuccess;
-    if (M > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    if (!launch_fits(M, 256)) return hipErrorInvalidValue;
     const int64_t chunks = (K + 2047) / 2048;   // 16-byte loads per thread
     const dim3 grid((unsigned)M), block(256);
     if (K % 8 != 0 || ldx % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15u) != 0)

@@ -57,7 +57,10 @@ typedef enum bi8_status {
     BI8_ERR_HIP = 5     /* a HIP runtime call failed                            */
 } bi8_status;
 
-/* Largest K accepted (elements); M, N and R are bounded by 2^31 - 1. */
+/* Largest K accepted (elements); M, N and R are bounded by 2^31 - 1.  A launch
+ * holds fewer than 2^32 threads: sizes that need more (2^26 rows of a quantiser,
+ * 2^24 of the per-token one, 2^23 tiles of a product or 2^27 columns of one with
+ * few rows) get BI8_ERR_HIP, "invalid argument", and are not launched. */
 #define BI8_MAX_K (1 << 23)
 
 /* Static, never-NULL name of a status code. */

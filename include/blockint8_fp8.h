@@ -96,7 +96,9 @@ int32_t blockint8_quant_weight_fp8(const uint16_t *w, int64_t N, int64_t K, int6
  *   workspace_bytes  its size
  *
  * Any M, N and K (K <= BI8_MAX_K); with K % 16 != 0 rows start at any byte and
- * a slower kernel runs.  Errors: as blockint8_gemm_ws, blocks [128, 128] only.
+ * a slower kernel runs.  Products of 2^23 tiles or more are not launched (the
+ * bound that blockint8.h gives beside BI8_MAX_K; the quantisers and the norm have
+ * none).  Errors: as blockint8_gemm_ws, blocks [128, 128] only.
  */
 int32_t blockint8_gemm_fp8(const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws, const uint16_t *bias,
                            uint16_t *y, int64_t M, int64_t N, int64_t K, int32_t block_n, int32_t block_k,
