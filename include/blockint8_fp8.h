@@ -164,12 +164,15 @@ int32_t blockint8_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, co
                                           void *stream);
 
 /*
- * The whole MoE layer in one call, six or seven launches on the stream:
- * blockint8_moe_route of the logits, blockint8_quant_act_gather_fp8, the w13
- * GEMM with the gating (blockint8_moe_gemm_silu_quant_fp8 where the grouped GEMM
- * of that size runs 256 x 128 or 256 x 256 tiles and I % 128 == 0, else
- * blockint8_moe_gemm_fp8 and blockint8_silu_mul_quant_fp8), the w2 GEMM and
- * blockint8_moe_combine.  out equals those calls' exactly.
+ * The whole MoE layer in one call: blockint8_moe_route of the logits (two
+ * launches), blockint8_quant_act_gather_fp8, the w13 GEMM with the gating
+ * (blockint8_moe_gemm_silu_quant_fp8 where the grouped GEMM of that size runs
+ * 256 x 128 or 256 x 256 tiles and I % 128 == 0, else blockint8_moe_gemm_fp8 and
+ * blockint8_silu_mul_quant_fp8), the w2 GEMM and blockint8_moe_combine: six
+ * launches, or seven where the gating is one of its own, and one more for each
+ * grouped GEMM that splits a partial round over K.  Those have their part of the
+ * layer's workspace: out equals the separate calls' exactly where each
+ * blockint8_moe_gemm_fp8 among them gets a workspace of its size.
  *
  *   x       bf16 [T, ldx], the first H columns of each row (2-byte aligned)
  *   logits  fp32 [T, E]
