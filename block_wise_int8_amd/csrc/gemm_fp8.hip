@@ -508,18 +508,22 @@ __device__ __forceinline__ void wait_lds() {
 // zero through the buffer range check, on both sides (a NaN code times zero
 // would be NaN).
 //
-// These tiles serve grids that leave a workgroup alone on its CU, where a block
-// takes as long as its chain of waits.  So a step reads the fragments of block
-// kb + 1 into a second set of registers while the matrix core works on block
-// kb, whose stage is refilled at once with block kb + NS; a sub-tile's sum is
-// rescaled behind the next one's MFMAs.  One barrier a block.
+// These tiles serve grids that leave a workgroup alone on its CU, where nothing
+// else fills its waits.  So a step reads the fragments of block kb + 1 into a
+// second set of registers while the matrix core works on block kb, whose stage is
+// refilled at once with block kb + NS; a sub-tile's sum is rescaled behind the
+// next one's MFMAs.  One barrier a block.
 // The activation scales reach LDS eight blocks at a time; the weight scale of
 // a wave's 128-row block is a scalar load a block ahead.
 //
-// Bound by that chain: 0.5 us a block with 128 x 64 tiles, whose MFMAs take a
-// quarter of it.  Measured (us): 128 x 64 333 x 5000 x 4000 21.9, 512 x 4096 x
-// 4096 18.1; 128 x 128 1024 x 4096 x 4096 25.5, grouped 512 x 4096 x 14336 over 8
-// experts 97.
+// Bound by two things, in us a block of 128 x 64 (128 x 128) tiles: 0.30 (0.48) is
+// one workgroup's own time on an idle chip, with 757 cycles near the sum of its
+// MFMAs (256 a SIMD), fragment reads (273 of the LDS) and fills (24 KB, 192 at 128
+// bytes a cycle).  The rest comes with the number of busy CUs, at the same clock,
+// and so from the path of the fills that they share: nothing up to 64 CUs, 0.41
+// (0.62) with 256 that share operands, 0.56 (0.70) with weights of their own.
+// Measured (us): 128 x 64 333 x 5000 x 4000 21.9, 512 x 4096 x 4096 18.1; 128 x 128
+// 1024 x 4096 x 4096 25.5, grouped 512 x 4096 x 14336 over 8 experts 97.
 template <int WN_, int WM_, int SA_, int SB_, int NS_>
 struct Cfg {
     static constexpr int WN = WN_, WM = WM_, SA = SA_, SB = SB_, NS = NS_;
