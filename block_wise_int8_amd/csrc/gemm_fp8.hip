@@ -1567,9 +1567,10 @@ hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
 // weight's stream beside them; split over K, a unit walks its share of the blocks,
 // and the partial sums are written and read once.  The choice is the smallest
 // estimate.  The constants are fitted to 700 products of sizes drawn over 1 to 8192
-// rows, 64 to 28672 columns, K 128 to 14336 and up to 64 experts, where the chosen
-// kernel takes 0.3 % (dense) and 0.8 % (grouped) longer than the fastest of the
-// five on average.
+// rows, 64 to 28672 columns, K 128 to 14336 and up to 64 experts
+// (profiles/e4m3_gemm_choice.csv), where the chosen kernel takes 0.3 % (dense) and
+// 0.9 % (grouped) longer than the fastest of the five on average; 0.7 % and 0.8 % on
+// 500 others.
 struct Tiling {
     Fp8Path path;
     int bn, bm;
