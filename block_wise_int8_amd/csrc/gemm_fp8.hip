@@ -1623,10 +1623,10 @@ bool odd_rows_streamed(int64_t M, int64_t N) { return N * (16 + M) <= 1000000; }
 // partial: bytes of fp32 partial sums that may be used (0: no split).
 // The streaming kernel reads the activations again for every 16 weight rows, and
 // for more than 16 tokens a CU holds one workgroup, not two.  Measured (streaming /
-// 128 x 64, us, weights from HBM, K = 4096): M = 1, N = 131072 91 / 117, M = 16, N =
-// 28672 31.2 / 30.8, M = 32, N = 14336 31 / 22.4, M = 64, N = 4096 16.0 / 18.9 (13.1
-// split over K), M = 64, N = K = 2048 15.4 / 9.8, M = 16, N = 8192, K = 28672 71 / 98
-// (47 split).
+// 128 x 64, us, weights from HBM, K = 4096): M = 1, N = 131072 91 / 116, M = 16, N =
+// 28672 31.5 / 29.7, M = 32, N = 14336 31.1 / 19.0 (17.7 split over K), M = 64, N =
+// 4096 16.1 / 18.4 (13.1 split), M = 64, N = K = 2048 15.4 / 9.8, M = 16, N = 8192, K =
+// 28672 71 / 98 (47 split).
 Choice choose_dense(int64_t M, int64_t N, int64_t K, int64_t partial) {
     Choice best;
     const double bytes = (double)N * (double)K;

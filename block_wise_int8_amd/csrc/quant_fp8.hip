@@ -7,7 +7,8 @@
 // Each is one pass over its input and bound by HBM: 2 B read and 1 B written
 // an element (the gating 4 and 1), 4 B a group.  Measured: activations 1 x 4096
 // 2.1 us, 2048 x 14336 16.0 us (5.5 TB/s), 16384 x 4096 32 us (6.3); gating 8192 x
-// 14336 106 us (5.5); weights, which are quantised once, 28672 x 4096 125 us.
+// 14336 106 us (5.5); weights, which are quantised once, 28672 x 4096 125 us (2.8
+// TB/s: a load touches 64 lines, two threads a row).
 #include "codes.hpp"
 #include "internal.hpp"
 
