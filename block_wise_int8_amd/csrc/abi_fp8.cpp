@@ -92,7 +92,7 @@ int32_t check_experts(const char *fn, int32_t E) {
 }
 
 int32_t check_variant(const char *fn, int32_t variant, int64_t K) {
-    if (variant < BI8_GEMM_AUTO || variant > BI8_GEMM_TILE_128X128)
+    if (variant < BI8_GEMM_AUTO || (variant > BI8_GEMM_TILE_128X128 && variant != BI8_GEMM_TILE_256X128_F16))
         return fail_status(BI8_ERR_SHAPE, "%s: unknown kernel variant %d", fn, variant);
     if (K % 16 != 0 && variant != BI8_GEMM_AUTO)
         return fail_status(BI8_ERR_ALIGN, "%s: K = %lld is not a multiple of 16; that form has one kernel (variant "
@@ -130,13 +130,13 @@ int32_t rmsnorm_quant(const char *fn, bool fp8, const uint16_t *x, int64_t ldx, 
 // The layer's workspace: parts at multiples of 256 bytes.  The w13 GEMM's output
 // and the w2 GEMM's share one (the first is read before the second is written).
 struct LayerPlan {
-    bool gated;   // w13 and the gating in one launch
+    bool gated;   // w13 and the gating in one launch (f16: by that variant, wherever I allows it)
     int64_t ids, weights, sorted_token, offsets, row_of, xq, xs, h, aq, as, partial, partial_bytes, bytes;
-    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, bool f16 = false) {
         const int64_t R = T * k, HB = (H + 127) / 128, IB = (I + 127) / 128;
         const bi8::Fp8Path path = bi8::select_moe_gemm_fp8_path(R, 2 * I, H, E);
-        gated = I % 128 == 0 && (path == bi8::Fp8Path::kTile256x128 || path == bi8::Fp8Path::kTile256x256);
-        const int64_t p13 = gated ? 0 : bi8::moe_gemm_fp8_workspace_bytes(R, 2 * I, H, E);
+        gated = I % 128 == 0 && (f16 || path == bi8::Fp8Path::kTile256x128 || path == bi8::Fp8Path::kTile256x256);
+        const int64_t p13 = gated || f16 ? 0 : bi8::moe_gemm_fp8_workspace_bytes(R, 2 * I, H, E);
         const int64_t p2 = bi8::moe_gemm_fp8_workspace_bytes(R, H, I, E);
         partial_bytes = p13 > p2 ? p13 : p2;
         const int64_t wide = !gated && 2 * I > H ? 2 * I : H;
@@ -344,7 +344,7 @@ int32_t blockint8_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, co
     BI8_TRY(check_align(fn, "w13", w13, 16));
     BI8_TRY(check_align(fn, "ws13", ws13, 4));
     return bi8::call_status(fn, bi8::launch_moe_gemm_silu_quant_fp8(xq, xs, expert_offsets, w13, ws13, aq, as, R, I, K,
-                                                                    E, static_cast<hipStream_t>(stream)));
+                                                                    E, false, static_cast<hipStream_t>(stream)));
 }
 
 int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, int32_t E) {
@@ -365,7 +365,19 @@ int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *log
                                 const float *ws13, const uint8_t *w2, const float *ws2, uint16_t *out, int64_t T,
                                 int64_t H, int64_t I, int32_t E, int32_t k, int32_t renormalize, int32_t block_n,
                                 int32_t block_k, void *workspace, int64_t workspace_bytes, void *stream) {
+    return blockint8_moe_layer_fp8_variant(BI8_GEMM_AUTO, x, ldx, logits, w13, ws13, w2, ws2, out, T, H, I, E, k,
+                                           renormalize, block_n, block_k, workspace, workspace_bytes, stream);
+}
+
+int32_t blockint8_moe_layer_fp8_variant(int32_t variant, const uint16_t *x, int64_t ldx, const float *logits,
+                                        const uint8_t *w13, const float *ws13, const uint8_t *w2, const float *ws2,
+                                        uint16_t *out, int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
+                                        int32_t renormalize, int32_t block_n, int32_t block_k, void *workspace,
+                                        int64_t workspace_bytes, void *stream) {
     static const char fn[] = "blockint8_moe_layer_fp8";
+    const bool f16 = variant == BI8_GEMM_TILE_256X128_F16;
+    if (variant != BI8_GEMM_AUTO && !f16)
+        return fail_status(BI8_ERR_SHAPE, "%s: variant %d is not one of the layer's", fn, variant);
     BI8_TRY(check_layer(fn, T, H, I, E, k));
     BI8_TRY(check_pitch(fn, "ldx", ldx, H));
     BI8_TRY(check_block(fn, block_n, block_k));
@@ -379,7 +391,7 @@ int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *log
     BI8_TRY(check_align(fn, "ws2", ws2, 4));
     BI8_TRY(check_align(fn, "out", out, 16));
     BI8_TRY(check_align(fn, "workspace", workspace, 256));
-    const LayerPlan p(T, H, I, E, k);
+    const LayerPlan p(T, H, I, E, k, f16);
     if (workspace_bytes < p.bytes)
         return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
                            (long long)p.bytes);
@@ -398,11 +410,11 @@ int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *log
     if (p.gated) {
         if (e == hipSuccess)
             e = bi8::launch_moe_gemm_silu_quant_fp8(u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, u8(p.aq), f32(p.as),
-                                                    R, I, H, E, st);
+                                                    R, I, H, E, f16, st);
     } else {
         if (e == hipSuccess)
-            e = bi8::launch_moe_gemm_fp8(bi8::Fp8Path::kAuto, u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, h, R,
-                                         2 * I, H, E, partial, p.partial_bytes, st);
+            e = bi8::launch_moe_gemm_fp8(f16 ? bi8::Fp8Path::kTile256x128F16 : bi8::Fp8Path::kAuto, u8(p.xq), f32(p.xs),
+                                         i32(p.offsets), w13, ws13, h, R, 2 * I, H, E, partial, p.partial_bytes, st);
         if (e == hipSuccess) e = bi8::launch_silu_mul_quant_fp8(h, R, I, u8(p.aq), f32(p.as), nullptr, st);
     }
     if (e == hipSuccess)

@@ -92,7 +92,8 @@ hipError_t launch_silu_mul_quant_fp8(const uint16_t *h, int64_t R, int64_t I, ui
                                      uint16_t *a_out, hipStream_t stream);
 hipError_t launch_quant_weight_fp8(const uint16_t *w, int64_t N, int64_t K, int64_t ldw, uint8_t *wq, float *ws,
                                    hipStream_t stream);
-enum class Fp8Path : int { kAuto = 0, kSkinny = 1, kTile128x64 = 2, kTile256x128 = 3, kTile256x256 = 4, kTile128x128 = 5 };
+enum class Fp8Path : int { kAuto = 0, kSkinny = 1, kTile128x64 = 2, kTile256x128 = 3, kTile256x256 = 4, kTile128x128 = 5,
+                            kTile256x128F16 = 8 };
 Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K);
 Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E);
 int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
@@ -102,7 +103,7 @@ hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, con
 int64_t moe_gemm_fp8_workspace_bytes(int64_t R, int64_t N, int64_t K, int32_t E);
 hipError_t launch_moe_gemm_silu_quant_fp8(const uint8_t *xq, const float *xs, const int32_t *offsets,
                                           const uint8_t *w13, const float *ws13, uint8_t *aq, float *as, int64_t R,
-                                          int64_t I, int64_t K, int32_t E, hipStream_t stream);
+                                          int64_t I, int64_t K, int32_t E, bool f16, hipStream_t stream);
 hipError_t launch_moe_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const int32_t *offsets,
                                const uint8_t *w, const float *ws, uint16_t *y, int64_t R, int64_t N, int64_t K,
                                int32_t E, float *workspace, int64_t workspace_bytes, hipStream_t stream);

@@ -6,7 +6,8 @@ of int8 ones: the same shapes, scales, blocks ([128, 128]) and errors.
 Products are summed in binary32 but for the matrix core's own sums of eight
 consecutive products, which it aligns to the largest and cuts 2^-13 below its
 leading bit (0.0003 of a product's output in norm, against the 0.0017 of its
-rounding to bf16; 0.0034 of the MoE layer's, 0.0019 without).
+rounding to bf16; 0.0034 of the MoE layer's, 0.0019 without).  The variant
+GEMM_TILE_256X128_F16 holds every sum in binary32, at half the matrix rate.
 """
 from __future__ import annotations
 
@@ -19,10 +20,12 @@ from . import _call as c
 __all__ = ["quant_act_fp8", "quant_act_gather_fp8", "silu_mul_quant_fp8", "quant_weight_fp8", "gemm_fp8",
            "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_silu_quant_fp8",
            "moe_gemm_fp8_workspace_size", "gemm_fp8_select", "moe_gemm_fp8_select", "moe_layer_fp8",
-           "moe_layer_fp8_workspace_size", "GEMM_TILE_128X128"]
+           "moe_layer_fp8_workspace_size", "GEMM_TILE_128X128", "GEMM_TILE_256X128_F16"]
 
 FP8 = torch.float8_e4m3fn
-GEMM_TILE_128X128 = 5   # the kernel variant that the int8 GEMM does not have
+# kernel variants that the int8 GEMM does not have
+GEMM_TILE_128X128 = 5
+GEMM_TILE_256X128_F16 = 8   # the codes multiplied as f16 values
 
 
 def declare(lib) -> None:
@@ -38,6 +41,7 @@ def declare(lib) -> None:
     c.declare(lib, "blockint8_moe_gemm_silu_quant_fp8", [vp] * 7 + [i64, i64, i64, i32, i32, i32, vp])
     c.declare(lib, "blockint8_moe_layer_fp8", [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, vp,
                                                i64, vp])
+    c.declare(lib, "blockint8_moe_layer_fp8_variant", [i32] + lib.blockint8_moe_layer_fp8.argtypes)
     c.declare(lib, "blockint8_moe_layer_fp8_workspace_size", [i64, i64, i64, i32, i32], i64)
     c.declare(lib, "blockint8_gemm_fp8_variant", [i32] + lib.blockint8_gemm_fp8.argtypes)
     c.declare(lib, "blockint8_moe_gemm_fp8_variant", [i32] + lib.blockint8_moe_gemm_fp8.argtypes)
@@ -229,7 +233,7 @@ def moe_layer_fp8_workspace_size(T: int, H: int, I: int, E: int, k: int) -> int:
 
 def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor, w2: torch.Tensor,
                   ws2: torch.Tensor, k: int, renormalize: bool = False, out: torch.Tensor | None = None,
-                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+                  workspace: torch.Tensor | None = None, variant: int | None = None) -> torch.Tensor:
     """The e4m3 FusedMoE layer on the GPU, through one C call: route, gather +
     quantise, w13 grouped GEMM, SiLU gating + quantise, w2 grouped GEMM,
     weighted combine.  Where the w13 GEMM runs 256-row weight tiles and
@@ -238,7 +242,9 @@ def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13
     float8_e4m3fn [E, H, I]; H and I multiples of 16.  ``workspace``: a
     contiguous, 256-byte aligned tensor of any type on the device, of
     ``moe_layer_fp8_workspace_size`` bytes or more (a fresh one when not
-    given); calls that share one must not overlap in time.  Returns bf16 [T, H]."""
+    given); calls that share one must not overlap in time.  ``variant``
+    GEMM_TILE_256X128_F16 holds the w13 GEMM's sums in binary32, which the second
+    quantiser reads.  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
     T, H, ldx = c.rows(x, "x", dev)
     rows, E = c.matrix(logits, "logits", dev, torch.float32)
@@ -258,7 +264,7 @@ def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13
         workspace = torch.empty(lib.blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k), dtype=torch.uint8,
                                 device=dev)
     wsp, nbytes = c.scratch(workspace, dev)
-    _bi8._check(c.call(lib.blockint8_moe_layer_fp8, dev, x.data_ptr(), ldx, logits.data_ptr(), w13.data_ptr(),
-                       ws13.data_ptr(), w2.data_ptr(), ws2.data_ptr(), out.data_ptr(), T, H, I, E, k,
+    _bi8._check(c.call(lib.blockint8_moe_layer_fp8_variant, dev, variant or 0, x.data_ptr(), ldx, logits.data_ptr(),
+                       w13.data_ptr(), ws13.data_ptr(), w2.data_ptr(), ws2.data_ptr(), out.data_ptr(), T, H, I, E, k,
                        1 if renormalize else 0, 128, 128, wsp, nbytes))
     return out

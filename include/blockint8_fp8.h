@@ -205,9 +205,21 @@ int64_t blockint8_moe_layer_fp8_workspace_size(int64_t T, int64_t H, int64_t I, 
  * alone), with the same arguments, results and errors.  Every
  * variant runs every size with K % 16 == 0, dense and grouped; with K % 16 != 0
  * only BI8_GEMM_AUTO is accepted (BI8_ERR_ALIGN otherwise).  An unknown variant
- * is BI8_ERR_SHAPE.  The ids are those of blockint8.h and one more.
+ * is BI8_ERR_SHAPE.  The ids are those of blockint8.h and two more:
+ *
+ *   BI8_GEMM_TILE_128X128      128 weight rows x 128 activation rows
+ *   BI8_GEMM_TILE_256X128_F16  256 x 128, the codes multiplied as f16 values:
+ *                              every sum is held in binary32, without the matrix
+ *                              core's cut (see blockint8_gemm_fp8), at half its
+ *                              rate.  Never the automatic choice: for results
+ *                              that are quantised again.
+ *
+ * blockint8_moe_layer_fp8_variant is blockint8_moe_layer_fp8 with BI8_GEMM_AUTO or,
+ * for the w13 GEMM, whose result the layer quantises again, BI8_GEMM_TILE_256X128_F16
+ * (in one launch with the gating where I % 128 == 0); another id is BI8_ERR_SHAPE.
+ * The workspace is the same.
  */
-enum { BI8_GEMM_TILE_128X128 = 5 };
+enum { BI8_GEMM_TILE_128X128 = 5, BI8_GEMM_TILE_256X128_F16 = 8 };
 
 int32_t blockint8_gemm_fp8_select(int64_t M, int64_t N, int64_t K);
 
@@ -222,6 +234,12 @@ int32_t blockint8_moe_gemm_fp8_variant(int32_t variant, const uint8_t *xq, const
                                        const int32_t *expert_offsets, const uint8_t *w, const float *ws, uint16_t *y,
                                        int64_t R, int64_t N, int64_t K, int32_t E, int32_t block_n, int32_t block_k,
                                        void *workspace, int64_t workspace_bytes, void *stream);
+
+int32_t blockint8_moe_layer_fp8_variant(int32_t variant, const uint16_t *x, int64_t ldx, const float *logits,
+                                        const uint8_t *w13, const float *ws13, const uint8_t *w2, const float *ws2,
+                                        uint16_t *out, int64_t T, int64_t H, int64_t I, int32_t E, int32_t k,
+                                        int32_t renormalize, int32_t block_n, int32_t block_k, void *workspace,
+                                        int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
