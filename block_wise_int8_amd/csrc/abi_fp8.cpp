@@ -130,13 +130,17 @@ int32_t rmsnorm_quant(const char *fn, bool fp8, const uint16_t *x, int64_t ldx, 
 // The layer's workspace: parts at multiples of 256 bytes.  The w13 GEMM's output
 // and the w2 GEMM's share one (the first is read before the second is written).
 struct LayerPlan {
-    bool gated;   // w13 and the gating in one launch (f16: by that variant, wherever I allows it)
+    bi8::Fp8Path w13;   // kAuto, or the kernel that holds the sums (see select_layer_w13_path)
+    bool gated;         // w13 and the gating in one launch
     int64_t ids, weights, sorted_token, offsets, row_of, xq, xs, h, aq, as, partial, partial_bytes, bytes;
-    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, bool f16 = false) {
+    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t variant) {
         const int64_t R = T * k, HB = (H + 127) / 128, IB = (I + 127) / 128;
-        const bi8::Fp8Path path = bi8::select_moe_gemm_fp8_path(R, 2 * I, H, E);
-        gated = I % 128 == 0 && (f16 || path == bi8::Fp8Path::kTile256x128 || path == bi8::Fp8Path::kTile256x256);
-        const int64_t p13 = gated || f16 ? 0 : bi8::moe_gemm_fp8_workspace_bytes(R, 2 * I, H, E);
+        w13 = variant == BI8_GEMM_AUTO ? bi8::select_layer_w13_path(R, 2 * I, H, E) : static_cast<bi8::Fp8Path>(variant);
+        const bi8::Fp8Path path = w13 == bi8::Fp8Path::kAuto ? bi8::select_moe_gemm_fp8_path(R, 2 * I, H, E) : w13;
+        gated = I % 128 == 0 && (path == bi8::Fp8Path::kTile256x128F16 || path == bi8::Fp8Path::kTile256x128 ||
+                                 path == bi8::Fp8Path::kTile256x256);
+        const int64_t p13 =
+            gated || w13 != bi8::Fp8Path::kAuto ? 0 : bi8::moe_gemm_fp8_workspace_bytes(R, 2 * I, H, E);
         const int64_t p2 = bi8::moe_gemm_fp8_workspace_bytes(R, H, I, E);
         partial_bytes = p13 > p2 ? p13 : p2;
         const int64_t wide = !gated && 2 * I > H ? 2 * I : H;
@@ -358,7 +362,15 @@ int64_t blockint8_moe_layer_fp8_workspace_size(int64_t T, int64_t H, int64_t I, 
     if (E < 1 || E > 1024 || k < 1 || k > 8 || k > E || T <= 0 || T > kMaxRows / k || H <= 0 || H > BI8_MAX_K ||
         H % 16 != 0 || I <= 0 || I > BI8_MAX_K || I % 16 != 0)
         return 0;
-    return LayerPlan(T, H, I, E, k).bytes;
+    return LayerPlan(T, H, I, E, k, BI8_GEMM_AUTO).bytes;
+}
+
+int32_t blockint8_moe_layer_fp8_select(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+    if (blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k) == 0) return BI8_GEMM_AUTO;
+    const LayerPlan p(T, H, I, E, k, BI8_GEMM_AUTO);
+    if (p.w13 != bi8::Fp8Path::kAuto) return static_cast<int32_t>(p.w13);
+    if (!p.gated && bi8::moe_gemm_fp8_workspace_bytes(T * k, 2 * I, H, E) > 0) return BI8_GEMM_TILE_128X64;
+    return static_cast<int32_t>(bi8::select_moe_gemm_fp8_path(T * k, 2 * I, H, E));
 }
 
 int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *logits, const uint8_t *w13,
@@ -375,8 +387,7 @@ int32_t blockint8_moe_layer_fp8_variant(int32_t variant, const uint16_t *x, int6
                                         int32_t renormalize, int32_t block_n, int32_t block_k, void *workspace,
                                         int64_t workspace_bytes, void *stream) {
     static const char fn[] = "blockint8_moe_layer_fp8";
-    const bool f16 = variant == BI8_GEMM_TILE_256X128_F16;
-    if (variant != BI8_GEMM_AUTO && !f16)
+    if (variant != BI8_GEMM_AUTO && variant != BI8_GEMM_TILE_256X128_F16)
         return fail_status(BI8_ERR_SHAPE, "%s: variant %d is not one of the layer's", fn, variant);
     BI8_TRY(check_layer(fn, T, H, I, E, k));
     BI8_TRY(check_pitch(fn, "ldx", ldx, H));
@@ -391,7 +402,7 @@ int32_t blockint8_moe_layer_fp8_variant(int32_t variant, const uint16_t *x, int6
     BI8_TRY(check_align(fn, "ws2", ws2, 4));
     BI8_TRY(check_align(fn, "out", out, 16));
     BI8_TRY(check_align(fn, "workspace", workspace, 256));
-    const LayerPlan p(T, H, I, E, k, f16);
+    const LayerPlan p(T, H, I, E, k, variant);
     if (workspace_bytes < p.bytes)
         return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
                            (long long)p.bytes);
@@ -410,11 +421,11 @@ int32_t blockint8_moe_layer_fp8_variant(int32_t variant, const uint16_t *x, int6
     if (p.gated) {
         if (e == hipSuccess)
             e = bi8::launch_moe_gemm_silu_quant_fp8(u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, u8(p.aq), f32(p.as),
-                                                    R, I, H, E, f16, st);
+                                                    R, I, H, E, p.w13 == bi8::Fp8Path::kTile256x128F16, st);
     } else {
         if (e == hipSuccess)
-            e = bi8::launch_moe_gemm_fp8(f16 ? bi8::Fp8Path::kTile256x128F16 : bi8::Fp8Path::kAuto, u8(p.xq), f32(p.xs),
-                                         i32(p.offsets), w13, ws13, h, R, 2 * I, H, E, partial, p.partial_bytes, st);
+            e = bi8::launch_moe_gemm_fp8(p.w13, u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, h, R, 2 * I, H, E,
+                                         partial, p.partial_bytes, st);
         if (e == hipSuccess) e = bi8::launch_silu_mul_quant_fp8(h, R, I, u8(p.aq), f32(p.as), nullptr, st);
     }
     if (e == hipSuccess)

@@ -96,6 +96,7 @@ enum class Fp8Path : int { kAuto = 0, kSkinny = 1, kTile128x64 = 2, kTile256x128
                             kTile256x128F16 = 8 };
 Fp8Path select_gemm_fp8_path(int64_t M, int64_t N, int64_t K);
 Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E);
+Fp8Path select_layer_w13_path(int64_t R, int64_t N, int64_t K, int32_t E);
 int64_t gemm_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_fp8(Fp8Path path, const uint8_t *xq, const float *xs, const uint8_t *w, const float *ws,
                            const uint16_t *bias, uint16_t *y, int64_t M, int64_t N, int64_t K, float *workspace,

@@ -3,11 +3,13 @@
 The functions of the int8 layer with ``torch.float8_e4m3fn`` codes in the place
 of int8 ones: the same shapes, scales, blocks ([128, 128]) and errors.
 
-Products are summed in binary32 but for the matrix core's own sums of eight
-consecutive products, which it aligns to the largest and cuts 2^-13 below its
-leading bit (0.0003 of a product's output in norm, against the 0.0017 of its
-rounding to bf16; 0.0034 of the MoE layer's, 0.0019 without).  The variant
-GEMM_TILE_256X128_F16 holds every sum in binary32, at half the matrix rate.
+Products are summed in binary32 but, in the tiled kernels, for the matrix core's
+own sums of eight consecutive products, which it aligns to the largest and cuts
+2^-13 below its leading bit (0.0003 of a product's output in norm, against the
+0.0017 of its rounding to bf16).  The streaming kernel and the variant
+GEMM_TILE_256X128_F16 hold every sum, the latter at half the matrix rate; the MoE
+layer takes them for w13, whose result is quantised again, where the weights'
+stream bounds it (its output is then 0.0017 from the 64-bit evaluation, else 0.0034).
 """
 from __future__ import annotations
 
@@ -20,7 +22,7 @@ from . import _call as c
 __all__ = ["quant_act_fp8", "quant_act_gather_fp8", "silu_mul_quant_fp8", "quant_weight_fp8", "gemm_fp8",
            "gemm_fp8_workspace_size", "linear_fp8", "moe_gemm_fp8", "moe_gemm_silu_quant_fp8",
            "moe_gemm_fp8_workspace_size", "gemm_fp8_select", "moe_gemm_fp8_select", "moe_layer_fp8",
-           "moe_layer_fp8_workspace_size", "GEMM_TILE_128X128", "GEMM_TILE_256X128_F16"]
+           "moe_layer_fp8_workspace_size", "moe_layer_fp8_select", "GEMM_TILE_128X128", "GEMM_TILE_256X128_F16"]
 
 FP8 = torch.float8_e4m3fn
 # kernel variants that the int8 GEMM does not have
@@ -42,6 +44,7 @@ def declare(lib) -> None:
     c.declare(lib, "blockint8_moe_layer_fp8", [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, vp,
                                                i64, vp])
     c.declare(lib, "blockint8_moe_layer_fp8_variant", [i32] + lib.blockint8_moe_layer_fp8.argtypes)
+    c.declare(lib, "blockint8_moe_layer_fp8_select", [i64, i64, i64, i32, i32])
     c.declare(lib, "blockint8_moe_layer_fp8_workspace_size", [i64, i64, i64, i32, i32], i64)
     c.declare(lib, "blockint8_gemm_fp8_variant", [i32] + lib.blockint8_gemm_fp8.argtypes)
     c.declare(lib, "blockint8_moe_gemm_fp8_variant", [i32] + lib.blockint8_moe_gemm_fp8.argtypes)
@@ -231,20 +234,26 @@ def moe_layer_fp8_workspace_size(T: int, H: int, I: int, E: int, k: int) -> int:
     return int(_bi8.load().blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k))
 
 
+def moe_layer_fp8_select(T: int, H: int, I: int, E: int, k: int) -> int:
+    """The kernel variant (``GEMM_*``) that ``moe_layer_fp8`` runs for the w13 GEMM (0 for sizes it rejects)."""
+    return int(_bi8.load().blockint8_moe_layer_fp8_select(T, H, I, E, k))
+
+
 def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor, w2: torch.Tensor,
                   ws2: torch.Tensor, k: int, renormalize: bool = False, out: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, variant: int | None = None) -> torch.Tensor:
     """The e4m3 FusedMoE layer on the GPU, through one C call: route, gather +
-    quantise, w13 grouped GEMM, SiLU gating + quantise, w2 grouped GEMM,
-    weighted combine.  Where the w13 GEMM runs 256-row weight tiles and
-    I % 128 == 0, it and the gating are one launch (moe_gemm_silu_quant_fp8).
+    quantise, w13 grouped GEMM (moe_layer_fp8_select), SiLU gating + quantise,
+    w2 grouped GEMM, weighted combine.  Where the w13 GEMM runs 256-row weight
+    tiles and I % 128 == 0, it and the gating are one launch
+    (moe_gemm_silu_quant_fp8).
     x bf16 [T, H]; logits fp32 [T, E]; w13 float8_e4m3fn [E, 2I, H]; w2
     float8_e4m3fn [E, H, I]; H and I multiples of 16.  ``workspace``: a
     contiguous, 256-byte aligned tensor of any type on the device, of
     ``moe_layer_fp8_workspace_size`` bytes or more (a fresh one when not
     given); calls that share one must not overlap in time.  ``variant``
-    GEMM_TILE_256X128_F16 holds the w13 GEMM's sums in binary32, which the second
-    quantiser reads.  Returns bf16 [T, H]."""
+    GEMM_TILE_256X128_F16 holds the w13 GEMM's sums, which the second quantiser
+    reads, whatever its size.  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
     T, H, ldx = c.rows(x, "x", dev)
     rows, E = c.matrix(logits, "logits", dev, torch.float32)

@@ -27,3 +27,13 @@ def test_rules(name, variant, kw, status):
 def test_the_int8_products_do_not_have_it():
     P = 0x10000
     assert bi8.load().blockint8_gemm_variant(F16, P, P, P, P, None, P, 4, 256, 256, 128, 128, None) == SHAPE
+
+
+def test_layer_select():
+    for bad in ((0, 256, 256, 8, 2), (4, 250, 256, 8, 2), (4, 256, 256, 8, 9), (1 << 31, 256, 256, 8, 2)):
+        assert bi8.moe_layer_fp8_select(*bad) == 0
+    # a token, a batch and a prompt of a layer with large weights; a small layer
+    assert bi8.moe_layer_fp8_select(1, 4096, 14336, 8, 2) == bi8.GEMM_SKINNY
+    assert bi8.moe_layer_fp8_select(256, 4096, 14336, 8, 2) == F16
+    assert bi8.moe_layer_fp8_select(4096, 4096, 14336, 8, 2) == bi8.GEMM_TILE_256X256
+    assert bi8.moe_layer_fp8_select(300, 512, 384, 4, 2) == bi8.GEMM_TILE_128X64

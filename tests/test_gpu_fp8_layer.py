@@ -21,9 +21,11 @@ def stages(x, logits, w13, s13, w2, s2, k, renormalize=False):
     I = N // 2
     _, weights, order, off, row_of = bi8.moe_route(logits, k, renormalize)
     xq, xs = bi8.quant_act_gather_fp8(x, order)
-    n13 = 0
-    if I % 128 == 0 and bi8.moe_gemm_fp8_select(T * k, N, H, E) in (bi8.GEMM_TILE_256X128, bi8.GEMM_TILE_256X256):
+    n13, w13_runs = 0, bi8.moe_layer_fp8_select(T, H, I, E, k)
+    if I % 128 == 0 and w13_runs in (bi8.GEMM_TILE_256X128, bi8.GEMM_TILE_256X256):
         aq, as_ = bi8.moe_gemm_silu_quant_fp8(xq, xs, off, w13, s13)
+    elif w13_runs in (bi8.GEMM_SKINNY, bi8.GEMM_TILE_256X128_F16):
+        aq, as_ = bi8.silu_mul_quant_fp8(bi8.moe_gemm_fp8(xq, xs, off, w13, s13, variant=w13_runs))
     else:
         n13 = bi8.moe_gemm_fp8_workspace_size(T * k, N, H, E)
         aq, as_ = bi8.silu_mul_quant_fp8(bi8.moe_gemm_fp8(xq, xs, off, w13, s13, workspace=scratch(n13)))
@@ -52,7 +54,7 @@ def layer_case(seed, T, E, H, I):
 
 
 # (T, E, H, I, k), which product splits K
-SPLIT = [(100, 2, 1024, 4096, 1, "w2"), (62, 3, 3456, 128, 2, "w13"), (227, 2, 3456, 544, 1, "w13"),
+SPLIT = [(100, 2, 1024, 4096, 1, "w2"), (62, 3, 3456, 128, 2, ""), (227, 2, 3456, 544, 1, "w13"),
          (42, 1, 5600, 3280, 1, "w13 w2"), (1, 64, 1024, 384, 8, ""), (8, 256, 512, 256, 8, ""), (3, 130, 256, 400, 2, "")]
 
 

@@ -1,4 +1,5 @@
-"""The e4m3 products whose sums binary32 holds (GEMM_TILE_256X128_F16).
+"""The e4m3 products whose sums binary32 holds: the streaming kernel, GEMM_TILE_256X128_F16, and the layer's w13
+where it runs them.
 
 Exact cases hold what the f8 matrix instruction cuts off: runs of eight with products of 2^16 that cancel and others
 of 2^-2 to 2^4 that remain.  Every partial sum, in any order, is a multiple of 2^-2 below 2^22 (128 products of a
@@ -14,11 +15,12 @@ import oracle
 from gpu_util import bf16_bits, bf16_to_dev, device, to_dev
 from oracle import fp8
 from test_gpu_fp8 import check_product, codes_dev, grouped_case, product_case, run_grouped
-from test_gpu_fp8_layer import layer_case, scratch
+from test_gpu_fp8_layer import layer_case, scratch, stages
 
 pytestmark = pytest.mark.gpu
 
 F16 = bi8.GEMM_TILE_256X128_F16
+HOLD = [bi8.GEMM_SKINNY, F16]
 
 
 def cancelling(rng, M, N, K):
@@ -49,13 +51,21 @@ def gemm(xq, xs, w, ws, bias=None, **kw):
                         **kw)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (3, 260, 112), (65, 129, 128), (130, 300, 272), (257, 515, 1040),
-                                   (520, 700, 144), (300, 1030, 2320)])
-def test_dense(M, N, K):
+@pytest.mark.parametrize("variant", HOLD)
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (3, 260, 112), (20, 100, 4096), (40, 140, 1040), (65, 129, 128),
+                                   (130, 300, 272), (257, 515, 1040), (520, 700, 144), (300, 1030, 2320)])
+def test_dense(M, N, K, variant):
     c = exact_case((1, M, N, K), M, N, K)
-    assert np.array_equal(bf16_bits(gemm(*c, variant=F16)), want_bits(fp8.gemm_f64(*c)[0]))
+    assert np.array_equal(bf16_bits(gemm(*c, variant=variant)), want_bits(fp8.gemm_f64(*c)[0]))
     c = product_case((2, M, N, K), M, N, K, True)
-    check_product(gemm(*c, variant=F16), *fp8.gemm_f64(*c), K)
+    check_product(gemm(*c, variant=variant), *fp8.gemm_f64(*c), K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 24), (9, 100, 1000), (30, 260, 136), (70, 300, 4104)])
+def test_streamed_rows_off_the_16_byte_grid(M, N, K):
+    c = exact_case((7, M, N, K), M, N, K)
+    assert bi8.gemm_fp8_select(M, N, K) == bi8.GEMM_SKINNY
+    assert np.array_equal(bf16_bits(gemm(*c)), want_bits(fp8.gemm_f64(*c)[0]))
 
 
 def test_the_cut_that_it_avoids():
@@ -63,25 +73,27 @@ def test_the_cut_that_it_avoids():
     x, w = np.zeros((1, 128)), np.zeros((1, 128))
     x[0, :8], w[0, :8] = [256, 2, 2, 2, 2, 256, 2, 2], [256, 1, 1, 1, 1, -256, 1, 1]
     c = fp8.encode(x), np.ones((1, 1), np.float32), fp8.encode(w), np.ones((1, 1), np.float32)
-    assert gemm(*c, variant=F16).item() == 12.0
+    for v in (None, *HOLD):
+        assert gemm(*c, variant=v).item() == 12.0
     assert gemm(*c, variant=bi8.GEMM_TILE_256X128).item() == 0.0
 
 
 @pytest.mark.parametrize("segments,N,K", [([1], 16, 16), ([0, 3, 0, 5, 0], 130, 272), ([130, 7, 260, 0, 33], 640, 272),
                                           ([300, 1, 513], 520, 1168), ([1] * 70, 64, 144)])
-def test_grouped(segments, N, K):
+@pytest.mark.parametrize("variant", HOLD)
+def test_grouped(segments, N, K, variant):
     xq, xs, w, ws = exact_case((3, N, K), sum(segments), N, K, len(segments))
     off = np.concatenate([[0], np.cumsum(segments)]).astype(np.int32)
-    y = run_grouped(xq, xs, off, w, ws, variant=F16)
+    y = run_grouped(xq, xs, off, w, ws, variant=variant)
     assert np.array_equal(bf16_bits(y), want_bits(fp8.moe_gemm_f64(xq, xs, off, w, ws)[0]))
     c = grouped_case((4, N, K), segments, N, K)
-    check_product(run_grouped(*c, variant=F16), *fp8.moe_gemm_f64(*c), K)
+    check_product(run_grouped(*c, variant=variant), *fp8.moe_gemm_f64(*c), K)
     # rows behind the last segment stay
     n = sum(segments)
     off = off.copy()
     off[off > n - 1] = n - 1
     y = torch.full((n, N), 5.0, dtype=torch.bfloat16, device=device())
-    run_grouped(xq, xs, off, w, ws, variant=F16, y=y)
+    run_grouped(xq, xs, off, w, ws, variant=variant, y=y)
     assert torch.all(y[n - 1:] == 5.0)
 
 
@@ -142,6 +154,22 @@ def test_layer_in_a_replayed_graph():
         torch.cuda.synchronize()
         want = wide_stages(cases[r][0], cases[r][1], *w, k)
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)), "replay %d" % r
+
+
+# (T, E, H, I, k), what the layer runs for w13 by itself: weights of 60 MB and more, rows enough for tiles
+@pytest.mark.parametrize("T,E,H,I,k,w13", [(256, 64, 2048, 1024, 8, F16), (256, 64, 2048, 1008, 8, F16),
+                                           (40, 64, 2048, 1024, 8, bi8.GEMM_SKINNY), (3, 8, 1024, 512, 2, bi8.GEMM_SKINNY)])
+def test_layer_holds_its_sums_where_the_weights_bound_it(T, E, H, I, k, w13):
+    assert bi8.moe_layer_fp8_select(T, H, I, E, k) == w13
+    d = layer_case(61, T, E, H, I)
+    want = stages(*d, k)[0]
+    nbytes = bi8.moe_layer_fp8_workspace_size(T, H, I, E, k)
+    room = torch.full((nbytes + 4096,), 0xFF, dtype=torch.uint8, device=device())
+    for kw in (dict(workspace=room[:nbytes]), {}):
+        assert torch.equal(bi8.moe_layer_fp8(*d, k, **kw).view(torch.int16), want.view(torch.int16))
+    assert torch.all(room[nbytes:] == 0xFF)
+    if w13 == F16:
+        assert torch.equal(bi8.moe_layer_fp8(*d, k, variant=F16).view(torch.int16), want.view(torch.int16))
 
 
 def test_layer_refuses_other_variants():
