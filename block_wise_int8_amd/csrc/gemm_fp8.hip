@@ -1293,9 +1293,11 @@ struct PingPong128 {
 // the other side of a rounding moves a code by a whole step.  A cluster's weight
 // fragment is converted chunk by chunk between its MFMAs, the activations once a
 // block, in the memory phase, where the whole rescale then stands too.
-// Measured (this / the f8 kernel, us): grouped, 512 rows over 8 experts of 28672 x
-// 4096 242 / 208, 64 rows over 8 of them 221 / 196, 8192 rows 1698 / 1103; 2048 x
-// 4096 x 14336 204 / 123.
+// Bound by MFMAs (2048 cycles a block) and vector work that overlap in part: 1.3 us a
+// block on an idle chip, 1.7 with all CUs busy.
+// Measured (this / the f8 kernel, us): grouped, 8 experts of 28672 x 4096 with 8
+// rows each 208 / 194, 64 each 218 / 205, 54 to 79 each 237 / 191, 1024 each 1705 /
+// 1065; 2048 x 4096 x 14336 203 / 123.
 template <bool MOE, int64_t GM, bool SILU = false, bool WIDE = false>
 __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1788,10 +1790,11 @@ Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E) {
 // The layer's w13 GEMM feeds a second quantiser, where a sum cut by the f8 matrix
 // instruction moves codes by whole steps: the layer's output is then 0.0034 from the
 // 64-bit evaluation, 0.0017 otherwise.  So it takes a kernel that holds its sums
-// wherever the weights' stream leaves the matrix core that time: the streaming
-// kernel, or the F16 tiles where they take little longer than the stream.  Measured
-// (layer of 8 experts, H 4096, I 14336, top 2, f8 / F16 tiles, us): 64 tokens 285 /
-// 302, 256 tokens 317 / 345; 1024 tokens, left to the f8 tiles, 518 / 722.
+// wherever the weights' stream leaves the matrix core most of that time: the
+// streaming kernel, or the F16 tiles where they take little longer than the stream.
+// Measured (layer of 8 experts, H 4096, I 14336, top 2, f8 / F16 tiles, us): 64
+// tokens 285 / 302, 256 tokens 317 / 345; 1024 tokens, left to the f8 tiles, 518 /
+// 722, and small layers, whose f8 tiles take half the time of F16 ones.
 // kAuto: the grouped GEMM's own choice (whose streaming kernel holds them too).
 Fp8Path select_layer_w13_path(int64_t R, int64_t N, int64_t K, int32_t E) {
     const Grouped g(R, N, K, E);
