@@ -1293,11 +1293,12 @@ struct PingPong128 {
 // the other side of a rounding moves a code by a whole step.  A cluster's weight
 // fragment is converted chunk by chunk between its MFMAs, the activations once a
 // block, in the memory phase, where the whole rescale then stands too.
-// Bound by MFMAs (2048 cycles a block) and vector work that overlap in part: 1.3 us a
-// block on an idle chip, 1.7 with all CUs busy.
-// Measured (this / the f8 kernel, us): grouped, 8 experts of 28672 x 4096 with 8
-// rows each 208 / 194, 64 each 218 / 205, 54 to 79 each 237 / 191, 1024 each 1705 /
-// 1065; 2048 x 4096 x 14336 203 / 123.
+// Bound by MFMAs (2048 cycles a block) and vector work that overlap in part, 1.4 us a
+// block on an idle chip, and by the power cap with all CUs busy: 1.65 us, with or
+// without the conversions.
+// Measured (this / the f8 kernel, us): grouped, 8 experts of 28672 x 4096 with 12 to
+// 24 rows 185 / 179, 25 to 45 196 / 185, 54 to 79 231 / 189, 1024 each 1705 / 1065;
+// 2048 x 4096 x 14336 203 / 123.
 template <bool MOE, int64_t GM, bool SILU = false, bool WIDE = false>
 __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1316,7 +1317,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = wave >> 2, quarter = wave & 3;
-    const bool busy = 64 * group < t.rows;   // WIDE: a group without rows only fills and keeps the barriers
+    // WIDE, where the f16 MFMAs set the clock: none for sub-rows that have no rows (a
+    // group without any only fills and keeps the barriers)
+    const bool busy = 64 * group < t.rows, both = 64 * group + 32 < t.rows;
     const int64_t K = p.K;
     const int nkb = (int)p.KB;
 
@@ -1445,9 +1448,9 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
             fill_w(after, 1, 1, kb + 2);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (!WIDE || busy) {
-            rescale(a ^ 1, 0, 0, 16);
-            if constexpr (WIDE) rescale(a ^ 1, 1, 0, 16);
+        if (!WIDE || busy) rescale(a ^ 1, 0, 0, 16);
+        if constexpr (WIDE) {
+            if (both) rescale(a ^ 1, 1, 0, 16);
         }
         if constexpr (a == 0)
             wait_lds<7>();   // weight sub-rows 1 of this block, the activation rows of the next
@@ -1455,13 +1458,14 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
             wait_lds<8>();   // weight sub-rows 0 of the next block
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (WIDE && a == 0) {
-            if (!busy) return;
-#pragma unroll
-            for (int b = 0; b < SB; ++b) {
+            auto widen = [&](const int b) __attribute__((always_inline)) {
                 tb[b] = xsv[b] * wsv;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) xh[b][c] = to_f16x8(xf[2 * b][c / 2][2 * (c & 1)], xf[2 * b][c / 2][2 * (c & 1) + 1]);
-            }
+                for (int c = 0; c < 8; ++c)
+                    xh[b][c] = to_f16x8(xf[2 * b][c / 2][2 * (c & 1)], xf[2 * b][c / 2][2 * (c & 1) + 1]);
+            };
+            if (busy) widen(0);
+            if (both) widen(1);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -1469,14 +1473,19 @@ __global__ __launch_bounds__(512) void gemm_fp8_pingpong128_kernel(GemmArgs p) {
     auto math = [&](auto ac, auto setc) __attribute__((always_inline)) {
         constexpr int a = decltype(ac)::value, before = a ^ 1, x0 = decltype(setc)::value;
         if constexpr (WIDE) {
-            if (!busy) return;
+            auto products = [&](auto sub_rows) __attribute__((always_inline)) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const f16x8 wh = to_f16x8(wf[c / 2][2 * (c & 1)], wf[c / 2][2 * (c & 1) + 1]);
+                for (int c = 0; c < 8; ++c) {
+                    const f16x8 wh = to_f16x8(wf[c / 2][2 * (c & 1)], wf[c / 2][2 * (c & 1) + 1]);
 #pragma unroll
-                for (int b = 0; b < SB; ++b)
-                    acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wh, xh[b][c], c ? acc[b] : zero16, 0, 0, 0);
-            }
+                    for (int b = 0; b < decltype(sub_rows)::value; ++b)
+                        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wh, xh[b][c], c ? acc[b] : zero16, 0, 0, 0);
+                }
+            };
+            if (both)
+                products(std::integral_constant<int, 2>{});
+            else if (busy)
+                products(std::integral_constant<int, 1>{});
 #pragma unroll
             for (int b = 0; b < SB; ++b) asm volatile("" : "+v"(acc[b]));
             return;
@@ -1630,7 +1639,7 @@ hipError_t launch_path(Fp8Path path, const GemmArgs &p, hipStream_t stream) {
 // of a launch is its rounds of tiles, the last one's by how full it is, and the
 // weight's stream beside them; split over K, a unit walks its share of the blocks,
 // and the partial sums are written and read once.  The choice is the smallest
-// estimate.  The constants are fitted to 700 products of sizes drawn over 1 to 8192
+// estimate.  The constants are fitted to some 700 products of sizes drawn over 1 to 8192
 // rows, 64 to 28672 columns, K 128 to 14336 and up to 64 experts
 // (profiles/e4m3_gemm_choice.csv), where the chosen kernel takes 0.3 % (dense) and
 // 0.9 % (grouped) longer than the fastest of the five on average; 0.7 % and 0.8 % on
@@ -1793,8 +1802,8 @@ Fp8Path select_moe_gemm_fp8_path(int64_t R, int64_t N, int64_t K, int32_t E) {
 // wherever the weights' stream leaves the matrix core most of that time: the
 // streaming kernel, or the F16 tiles where they take little longer than the stream.
 // Measured (layer of 8 experts, H 4096, I 14336, top 2, f8 / F16 tiles, us): 64
-// tokens 285 / 302, 256 tokens 317 / 345; 1024 tokens, left to the f8 tiles, 518 /
-// 722, and small layers, whose f8 tiles take half the time of F16 ones.
+// tokens 285 / 300, 256 tokens 317 / 343; 1024 tokens, left to the f8 tiles, 518 /
+// 730, and small layers, whose f8 tiles take half the time of F16 ones.
 // kAuto: the grouped GEMM's own choice (whose streaming kernel holds them too).
 Fp8Path select_layer_w13_path(int64_t R, int64_t N, int64_t K, int32_t E) {
     const Grouped g(R, N, K, E);

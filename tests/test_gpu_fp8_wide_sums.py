@@ -61,6 +61,16 @@ def test_dense(M, N, K, variant):
     check_product(gemm(*c, variant=variant), *fp8.gemm_f64(*c), K)
 
 
+@pytest.mark.parametrize("M", [31, 32, 33, 63, 64, 66, 95, 96, 97, 128, 160, 161])
+def test_sub_rows_without_rows(M):
+    """The F16 tiles leave out 32-row sub-rows that have no rows: tiles that end on both sides of each."""
+    N, K = 300, 400
+    c = exact_case((8, M), M, N, K)
+    room = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device=device())
+    y = gemm(*c, variant=F16, y=room[: M * N].view(M, N))
+    assert np.array_equal(bf16_bits(y), want_bits(fp8.gemm_f64(*c)[0])) and torch.all(room[M * N:] == 7.0)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 40, 24), (9, 100, 1000), (30, 260, 136), (70, 300, 4104)])
 def test_streamed_rows_off_the_16_byte_grid(M, N, K):
     c = exact_case((7, M, N, K), M, N, K)
