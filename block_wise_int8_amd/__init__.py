@@ -18,6 +18,8 @@ Entry points (same names as the C ABI, without the ``blockint8_`` prefix):
   and :func:`moe_layer`, the whole FusedMoE layer built from them
 * :func:`rmsnorm_quant` -- residual addition, RMS norm and quantisation (int8
   or e4m3 codes), what feeds the linears and the MoE layer
+* :func:`qk_norm_rope` -- norm of query and key heads and their rotation by
+  position, what reads the query / key / value projection's output
 * :func:`quant_act_fp8`, :func:`gemm_fp8`, :func:`linear_fp8`,
   :func:`moe_gemm_fp8`, :func:`moe_layer_fp8`, ... -- the e4m3 form of the same
   layer (module :mod:`.fp8`)
@@ -111,6 +113,7 @@ def load() -> ctypes.CDLL:
         getattr(lib, f).restype = i32
     fp8.declare(lib)
     norm.declare(lib)
+    heads.declare(lib)
     _lib = lib
     return lib
 
@@ -584,8 +587,9 @@ def check_tp_partition(input_size: int, input_size_per_partition: int, output_pa
                                                len(output_partition_sizes), int(tp_size), block[0], block[1]))
 
 
-from . import fp8, norm  # noqa: E402  (they use the names above)
+from . import fp8, heads, norm  # noqa: E402  (they use the names above)
 from .fp8 import *  # noqa: E402,F401,F403
+from .heads import *  # noqa: E402,F401,F403
 from .norm import *  # noqa: E402,F401,F403
 
-__all__ += fp8.__all__ + norm.__all__
+__all__ += fp8.__all__ + norm.__all__ + heads.__all__

@@ -113,4 +113,21 @@ hipError_t launch_rmsnorm_quant(bool fp8, const uint16_t *x, int64_t ldx, const 
                                 const uint16_t *weight, double eps, int64_t M, int64_t H, uint16_t *h, int64_t ldh,
                                 uint16_t *y, void *xq, float *xs, hipStream_t stream);
 
+// Norm and rotation of query and key heads (heads.hip).
+constexpr int kMaxAxes = 4;
+struct HeadsArgs {
+    const uint16_t *q, *k;             // k: null with Hk = 0
+    const uint16_t *q_weight, *k_weight;   // null: no norm
+    uint16_t *q_out, *k_out;
+    const float *table;                // [P, rot]
+    const int32_t *positions;          // axis a at a * positions_axis
+    int64_t q_token, q_head, k_token, k_head, q_out_token, q_out_head, k_out_token, k_out_head;
+    int64_t P, positions_axis, T;
+    double eps;
+    int32_t Hq, Hk, D, rot, axes, interleaved;
+    int32_t first[kMaxAxes];           // first pair of each axis (unused axes: past every pair)
+    int32_t log_lanes, share, table_chunks;   // the launch's own
+};
+hipError_t launch_qk_norm_rope(HeadsArgs p, hipStream_t stream);
+
 }  // namespace bi8
