@@ -18,6 +18,8 @@ Entry points (same names as the C ABI, without the ``blockint8_`` prefix):
   and :func:`moe_layer`, the whole FusedMoE layer built from them
 * :func:`rmsnorm_quant` -- residual addition, RMS norm and quantisation (int8
   or e4m3 codes), what feeds the linears and the MoE layer
+* :func:`moe_route_grouped` -- the router with softmax or sigmoid scores, a bias
+  for balance and groups of experts; the MoE layers take its result as ``route``
 * :func:`qk_norm_rope` -- norm of query and key heads and their rotation by
   position, what reads the query / key / value projection's output
 * :func:`quant_act_fp8`, :func:`gemm_fp8`, :func:`linear_fp8`,
@@ -114,6 +116,7 @@ def load() -> ctypes.CDLL:
     fp8.declare(lib)
     norm.declare(lib)
     heads.declare(lib)
+    _route.declare(lib)
     _lib = lib
     return lib
 
@@ -535,15 +538,20 @@ def moe_combine(y2: torch.Tensor, row_of: torch.Tensor, topk_weights: torch.Tens
     return out
 
 
-def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor,
+def moe_layer(x: torch.Tensor, logits: torch.Tensor | None, w13: torch.Tensor, ws13: torch.Tensor,
               w2: torch.Tensor, ws2: torch.Tensor, k: int, renormalize: bool = False,
-              variant: int | None = None):
+              variant: int | None = None, route=None):
     """The block-wise INT8 FusedMoE layer on the GPU, one launch per step:
     route, gather + quantise, w13 grouped GEMM, SiLU gating + quantise, w2
     grouped GEMM, weighted combine.  With the default kernels and I % 128 == 0
     the w13 GEMM and the gating run as one launch (moe_gemm_silu_quant).  x bf16 [T, H]; logits fp32 [T, E];
-    w13 int8 [E, 2I, H]; w2 int8 [E, H, I].  Returns bf16 [T, H]."""
-    ids, w, st, off, row_of = moe_route(logits, k, renormalize)
+    w13 int8 [E, 2I, H]; w2 int8 [E, H, I].  Returns bf16 [T, H].  ``route``: the
+    five tensors of ``moe_route`` or ``moe_route_grouped`` with this k, in the place
+    of the logits (None then, and ``renormalize`` False)."""
+    if route is None:
+        ids, w, st, off, row_of = moe_route(logits, k, renormalize)
+    else:
+        w, st, off, row_of = _call.routing(route, x, logits, renormalize, w13.shape[0], k)
     xq, xs = quant_act_gather(x, st)
     if variant is None and (w13.shape[1] // 2) % BLOCK == 0:
         aq, as_ = moe_gemm_silu_quant(xq, xs, off, w13, ws13)
@@ -587,9 +595,10 @@ def check_tp_partition(input_size: int, input_size_per_partition: int, output_pa
                                                len(output_partition_sizes), int(tp_size), block[0], block[1]))
 
 
-from . import fp8, heads, norm  # noqa: E402  (they use the names above)
+from . import _call, fp8, heads, norm, route as _route  # noqa: E402  (they use the names above)
 from .fp8 import *  # noqa: E402,F401,F403
 from .heads import *  # noqa: E402,F401,F403
 from .norm import *  # noqa: E402,F401,F403
+from .route import *  # noqa: E402,F401,F403
 
-__all__ += fp8.__all__ + norm.__all__ + heads.__all__
+__all__ += fp8.__all__ + norm.__all__ + heads.__all__ + _route.__all__

@@ -105,6 +105,18 @@ def output(t, name: str, dev: int, dtype: torch.dtype, shape: tuple):
     return dense(t, name, dev, dtype, shape)
 
 
+def routing(route, x, logits, renormalize: bool, E: int, k: int):
+    """A given routing of x's tokens, checked: (topk_weights, sorted_token, expert_offsets, row_of)."""
+    if logits is not None or renormalize:
+        raise ValueError("a given routing takes no logits and is not renormalised")
+    dev, T = device_of(x, "x"), x.shape[0]
+    _, weights, sorted_token, offsets, row_of = route
+    return (dense(weights, "topk_weights", dev, torch.float32, (T, k)),
+            dense(sorted_token, "sorted_token", dev, torch.int32, (T * k,)),
+            dense(offsets, "expert_offsets", dev, torch.int32, (E + 1,)),
+            dense(row_of, "row_of", dev, torch.int32, (T, k)))
+
+
 def scratch(t, dev: int):
     """(pointer, bytes) of an optional workspace of any type."""
     if t is None:

@@ -8,6 +8,7 @@
 
 #include "../../include/blockint8_fp8.h"
 #include "../../include/blockint8_norm.h"
+#include "../../include/blockint8_route.h"
 #include "checks.hpp"
 #include "internal.hpp"
 
@@ -85,7 +86,7 @@ struct LayerPlan {
     bi8::Fp8Path w13;   // kAuto, or the kernel that holds the sums (see select_layer_w13_path)
     bool gated;         // w13 and the gating in one launch
     int64_t ids, weights, sorted_token, offsets, row_of, xq, xs, h, aq, as, partial, partial_bytes, bytes;
-    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t variant) {
+    LayerPlan(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t variant, bool routed = false) {
         const int64_t R = T * k, HB = (H + 127) / 128, IB = (I + 127) / 128;
         w13 = variant == BI8_GEMM_AUTO ? bi8::select_layer_w13_path(R, 2 * I, H, E) : static_cast<bi8::Fp8Path>(variant);
         const bi8::Fp8Path path = w13 == bi8::Fp8Path::kAuto ? bi8::select_moe_gemm_fp8_path(R, 2 * I, H, E) : w13;
@@ -102,11 +103,12 @@ struct LayerPlan {
             bytes += (n + 255) / 256 * 256;
             return at;
         };
-        ids = take(R * 4);
-        weights = take(R * 4);
-        sorted_token = take(R * 4);
-        offsets = take((E + 1) * 4);
-        row_of = take(R * 4);
+        const int64_t own = routed ? 0 : 1;   // the routing's, where it is not given
+        ids = take(own * R * 4);
+        weights = take(own * R * 4);
+        sorted_token = take(own * R * 4);
+        offsets = take(own * (E + 1) * 4);
+        row_of = take(own * R * 4);
         xq = take(R * H);
         xs = take(R * HB * 4);
         h = take(R * wide * 2);
@@ -116,9 +118,17 @@ struct LayerPlan {
     }
 };
 
-int32_t check_layer(const char *fn, int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+constexpr int32_t kMostTop = 8, kMostTopRouted = 32;
+
+bool layer_sizes_fit(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t most_k) {
+    return E >= 1 && E <= 1024 && k >= 1 && k <= most_k && k <= E && T > 0 && T <= kMaxRows / k && H > 0 &&
+           H <= BI8_MAX_K && H % 16 == 0 && I > 0 && I <= BI8_MAX_K && I % 16 == 0;
+}
+
+int32_t check_layer(const char *fn, int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, int32_t most_k) {
     if (E < 1 || E > 1024) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 1024]", fn, E);
-    if (k < 1 || k > 8 || k > E) return fail_status(BI8_ERR_SHAPE, "%s: k = %d out of range [1, min(E, 8)]", fn, k);
+    if (k < 1 || k > most_k || k > E)
+        return fail_status(BI8_ERR_SHAPE, "%s: k = %d out of range [1, min(E, %d)]", fn, k, most_k);
     if (T < 0 || T > kMaxRows / k)
         return fail_status(BI8_ERR_SHAPE, "%s: T = %lld out of range", fn, (long long)T);
     BI8_TRY(check_columns(fn, "H", H));
@@ -127,6 +137,52 @@ int32_t check_layer(const char *fn, int64_t T, int64_t H, int64_t I, int32_t E, 
         return fail_status(BI8_ERR_ALIGN, "%s: H = %lld and I = %lld must be multiples of 16", fn, (long long)H,
                            (long long)I);
     return BI8_OK;
+}
+
+// A routing: row r is token sorted_token[r], rows [offsets[e], offsets[e + 1]) are
+// expert e's, slot s of token t is row row_of[t, s] with weight weights[t, s].
+struct Routing {
+    const int32_t *sorted_token, *offsets, *row_of;
+    const float *weights;
+};
+
+int32_t check_layer_tensors(const char *fn, const uint16_t *x, const uint8_t *w13, const float *ws13, const uint8_t *w2,
+                            const float *ws2, const uint16_t *out, const void *workspace) {
+    if (!x || !w13 || !ws13 || !w2 || !ws2 || !out || !workspace) return null_pointer(fn);
+    BI8_TRY(check_align(fn, "x", x, 2));
+    BI8_TRY(check_align(fn, "w13", w13, 16));
+    BI8_TRY(check_align(fn, "ws13", ws13, 4));
+    BI8_TRY(check_align(fn, "w2", w2, 16));
+    BI8_TRY(check_align(fn, "ws2", ws2, 4));
+    BI8_TRY(check_align(fn, "out", out, 16));
+    return check_align(fn, "workspace", workspace, 256);
+}
+
+// The layer's launches behind the routing.
+hipError_t launch_layer(const LayerPlan &p, char *at, const Routing &route, const uint16_t *x, int64_t ldx,
+                        const uint8_t *w13, const float *ws13, const uint8_t *w2, const float *ws2, uint16_t *out,
+                        int64_t T, int64_t H, int64_t I, int32_t E, int32_t k, hipStream_t st) {
+    auto f32 = [at](int64_t off) { return reinterpret_cast<float *>(at + off); };
+    auto u8 = [at](int64_t off) { return reinterpret_cast<uint8_t *>(at + off); };
+    uint16_t *const h = reinterpret_cast<uint16_t *>(at + p.h);
+    float *const partial = p.partial_bytes ? f32(p.partial) : nullptr;
+    const int64_t R = T * k;
+    hipError_t e = bi8::launch_quant_act_fp8(x, T, ldx, route.sorted_token, R, H, u8(p.xq), f32(p.xs), st);
+    if (p.gated) {
+        if (e == hipSuccess)
+            e = bi8::launch_moe_gemm_silu_quant_fp8(u8(p.xq), f32(p.xs), route.offsets, w13, ws13, u8(p.aq), f32(p.as),
+                                                    R, I, H, E, p.w13 == bi8::Fp8Path::kTile256x128F16, st);
+    } else {
+        if (e == hipSuccess)
+            e = bi8::launch_moe_gemm_fp8(p.w13, u8(p.xq), f32(p.xs), route.offsets, w13, ws13, h, R, 2 * I, H, E,
+                                         partial, p.partial_bytes, st);
+        if (e == hipSuccess) e = bi8::launch_silu_mul_quant_fp8(h, R, I, u8(p.aq), f32(p.as), nullptr, st);
+    }
+    if (e == hipSuccess)
+        e = bi8::launch_moe_gemm_fp8(bi8::Fp8Path::kAuto, u8(p.aq), f32(p.as), route.offsets, w2, ws2, h, R, H, I, E,
+                                     partial, p.partial_bytes, st);
+    if (e == hipSuccess) e = bi8::launch_moe_combine(h, R, route.row_of, route.weights, T, k, H, out, st);
+    return e;
 }
 
 }  // namespace
@@ -311,10 +367,11 @@ int64_t blockint8_moe_gemm_fp8_workspace_size(int64_t R, int64_t N, int64_t K, i
 }
 
 int64_t blockint8_moe_layer_fp8_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
-    if (E < 1 || E > 1024 || k < 1 || k > 8 || k > E || T <= 0 || T > kMaxRows / k || H <= 0 || H > BI8_MAX_K ||
-        H % 16 != 0 || I <= 0 || I > BI8_MAX_K || I % 16 != 0)
-        return 0;
-    return LayerPlan(T, H, I, E, k, BI8_GEMM_AUTO).bytes;
+    return layer_sizes_fit(T, H, I, E, k, kMostTop) ? LayerPlan(T, H, I, E, k, BI8_GEMM_AUTO).bytes : 0;
+}
+
+int64_t blockint8_moe_layer_fp8_routed_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
+    return layer_sizes_fit(T, H, I, E, k, kMostTopRouted) ? LayerPlan(T, H, I, E, k, BI8_GEMM_AUTO, true).bytes : 0;
 }
 
 int32_t blockint8_moe_layer_fp8_select(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k) {
@@ -341,50 +398,55 @@ int32_t blockint8_moe_layer_fp8_variant(int32_t variant, const uint16_t *x, int6
     static const char fn[] = "blockint8_moe_layer_fp8";
     if (variant != BI8_GEMM_AUTO && variant != BI8_GEMM_TILE_256X128_F16)
         return fail_status(BI8_ERR_SHAPE, "%s: variant %d is not one of the layer's", fn, variant);
-    BI8_TRY(check_layer(fn, T, H, I, E, k));
+    BI8_TRY(check_layer(fn, T, H, I, E, k, kMostTop));
     BI8_TRY(check_pitch(fn, "ldx", ldx, H));
     BI8_TRY(check_block(fn, block_n, block_k));
     if (T == 0) return done(fn);
-    if (!x || !logits || !w13 || !ws13 || !w2 || !ws2 || !out || !workspace) return null_pointer(fn);
-    BI8_TRY(check_align(fn, "x", x, 2));
+    if (!logits) return null_pointer(fn);
+    BI8_TRY(check_layer_tensors(fn, x, w13, ws13, w2, ws2, out, workspace));
     BI8_TRY(check_align(fn, "logits", logits, 4));
-    BI8_TRY(check_align(fn, "w13", w13, 16));
-    BI8_TRY(check_align(fn, "ws13", ws13, 4));
-    BI8_TRY(check_align(fn, "w2", w2, 16));
-    BI8_TRY(check_align(fn, "ws2", ws2, 4));
-    BI8_TRY(check_align(fn, "out", out, 16));
-    BI8_TRY(check_align(fn, "workspace", workspace, 256));
     const LayerPlan p(T, H, I, E, k, variant);
     if (workspace_bytes < p.bytes)
         return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
                            (long long)p.bytes);
     char *const at = static_cast<char *>(workspace);
     auto i32 = [at](int64_t off) { return reinterpret_cast<int32_t *>(at + off); };
-    auto f32 = [at](int64_t off) { return reinterpret_cast<float *>(at + off); };
-    auto u8 = [at](int64_t off) { return reinterpret_cast<uint8_t *>(at + off); };
-    uint16_t *const h = reinterpret_cast<uint16_t *>(at + p.h);
-    float *const partial = p.partial_bytes ? f32(p.partial) : nullptr;
+    float *const weights = reinterpret_cast<float *>(at + p.weights);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const int64_t R = T * k;
-    hipError_t e = bi8::launch_moe_route(logits, T, E, k, renormalize, i32(p.ids), f32(p.weights), i32(p.sorted_token),
+    hipError_t e = bi8::launch_moe_route(logits, T, E, k, renormalize, i32(p.ids), weights, i32(p.sorted_token),
                                          i32(p.offsets), i32(p.row_of), st);
     if (e == hipSuccess)
-        e = bi8::launch_quant_act_fp8(x, T, ldx, i32(p.sorted_token), R, H, u8(p.xq), f32(p.xs), st);
-    if (p.gated) {
-        if (e == hipSuccess)
-            e = bi8::launch_moe_gemm_silu_quant_fp8(u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, u8(p.aq), f32(p.as),
-                                                    R, I, H, E, p.w13 == bi8::Fp8Path::kTile256x128F16, st);
-    } else {
-        if (e == hipSuccess)
-            e = bi8::launch_moe_gemm_fp8(p.w13, u8(p.xq), f32(p.xs), i32(p.offsets), w13, ws13, h, R, 2 * I, H, E,
-                                         partial, p.partial_bytes, st);
-        if (e == hipSuccess) e = bi8::launch_silu_mul_quant_fp8(h, R, I, u8(p.aq), f32(p.as), nullptr, st);
-    }
-    if (e == hipSuccess)
-        e = bi8::launch_moe_gemm_fp8(bi8::Fp8Path::kAuto, u8(p.aq), f32(p.as), i32(p.offsets), w2, ws2, h, R, H, I, E,
-                                     partial, p.partial_bytes, st);
-    if (e == hipSuccess) e = bi8::launch_moe_combine(h, R, i32(p.row_of), f32(p.weights), T, k, H, out, st);
+        e = launch_layer(p, at, {i32(p.sorted_token), i32(p.offsets), i32(p.row_of), weights}, x, ldx, w13, ws13, w2,
+                         ws2, out, T, H, I, E, k, st);
     return bi8::call_status(fn, e);
+}
+
+int32_t blockint8_moe_layer_fp8_routed(int32_t variant, const uint16_t *x, int64_t ldx, const float *topk_weights,
+                                       const int32_t *sorted_token, const int32_t *expert_offsets,
+                                       const int32_t *row_of, const uint8_t *w13, const float *ws13, const uint8_t *w2,
+                                       const float *ws2, uint16_t *out, int64_t T, int64_t H, int64_t I, int32_t E,
+                                       int32_t k, int32_t block_n, int32_t block_k, void *workspace,
+                                       int64_t workspace_bytes, void *stream) {
+    static const char fn[] = "blockint8_moe_layer_fp8_routed";
+    if (variant != BI8_GEMM_AUTO && variant != BI8_GEMM_TILE_256X128_F16)
+        return fail_status(BI8_ERR_SHAPE, "%s: variant %d is not one of the layer's", fn, variant);
+    BI8_TRY(check_layer(fn, T, H, I, E, k, kMostTopRouted));
+    BI8_TRY(check_pitch(fn, "ldx", ldx, H));
+    BI8_TRY(check_block(fn, block_n, block_k));
+    if (T == 0) return done(fn);
+    if (!topk_weights || !sorted_token || !expert_offsets || !row_of) return null_pointer(fn);
+    BI8_TRY(check_layer_tensors(fn, x, w13, ws13, w2, ws2, out, workspace));
+    BI8_TRY(check_align(fn, "topk_weights", topk_weights, 4));
+    BI8_TRY(check_align(fn, "sorted_token", sorted_token, 4));
+    BI8_TRY(check_align(fn, "expert_offsets", expert_offsets, 4));
+    BI8_TRY(check_align(fn, "row_of", row_of, 4));
+    const LayerPlan p(T, H, I, E, k, variant, true);
+    if (workspace_bytes < p.bytes)
+        return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
+                           (long long)p.bytes);
+    return bi8::call_status(fn, launch_layer(p, static_cast<char *>(workspace),
+                                             {sorted_token, expert_offsets, row_of, topk_weights}, x, ldx, w13, ws13,
+                                             w2, ws2, out, T, H, I, E, k, static_cast<hipStream_t>(stream)));
 }
 
 int32_t blockint8_rmsnorm_quant(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,

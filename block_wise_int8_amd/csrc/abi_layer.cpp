@@ -1,6 +1,6 @@
 // C ABI of the operators beside the 8-bit products: argument checks on the host,
-// then the launches on the caller's stream.  See include/blockint8_heads.h for the
-// contracts.
+// then the launches on the caller's stream.  See include/blockint8_heads.h and
+// include/blockint8_route.h for the contracts.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "../../include/blockint8_heads.h"
+#include "../../include/blockint8_route.h"
 #include "checks.hpp"
 #include "internal.hpp"
 
@@ -103,6 +104,54 @@ int32_t blockint8_qk_norm_rope(const uint16_t *q, int64_t q_token, int64_t q_hea
     p.table = table, p.P = P, p.positions = positions, p.positions_axis = positions_axis, p.axes = axes;
     p.eps = eps, p.T = T, p.Hq = Hq, p.Hk = Hk, p.D = D, p.rot = rot, p.interleaved = interleaved != 0;
     return bi8::call_status(fn, bi8::launch_qk_norm_rope(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t blockint8_moe_route_grouped_workspace_size(int64_t T, int32_t E) {
+    if (T <= 0 || T > kMaxRows || E < 1 || E > 1024) return 0;
+    return bi8::route_grouped_workspace_bytes(T, E);
+}
+
+int32_t blockint8_moe_route_grouped(const void *logits, int32_t logits_bf16, int64_t ldl, const float *bias, int64_t T,
+                                    int32_t E, int32_t k, int32_t score, int32_t groups, int32_t topk_groups,
+                                    int32_t group_top, int32_t renormalize, double scale, int32_t *topk_ids,
+                                    float *topk_weights, int32_t *sorted_token, int32_t *expert_offsets,
+                                    int32_t *row_of, void *workspace, int64_t workspace_bytes, void *stream) {
+    static const char fn[] = "blockint8_moe_route_grouped";
+    if (E < 1 || E > 1024) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 1024]", fn, E);
+    if (k < 1 || k > 32 || k > E) return fail_status(BI8_ERR_SHAPE, "%s: k = %d out of range [1, min(E, 32)]", fn, k);
+    if (T < 0 || T > kMaxRows / k) return fail_status(BI8_ERR_SHAPE, "%s: T = %lld out of range", fn, (long long)T);
+    if (score != BI8_SCORE_SOFTMAX && score != BI8_SCORE_SIGMOID)
+        return fail_status(BI8_ERR_SHAPE, "%s: unknown score %d", fn, score);
+    if (groups < 1 || groups > 64 || E % groups != 0)
+        return fail_status(BI8_ERR_SHAPE, "%s: groups = %d must divide E = %d, in [1, 64]", fn, groups, E);
+    if (topk_groups < 1 || topk_groups > groups || topk_groups * (E / groups) < k)
+        return fail_status(BI8_ERR_SHAPE, "%s: topk_groups = %d must be in [1, %d] and hold k = %d experts", fn,
+                           topk_groups, groups, k);
+    if (group_top != 1 && group_top != 2)
+        return fail_status(BI8_ERR_SHAPE, "%s: group_top = %d must be 1 or 2", fn, group_top);
+    if (!std::isfinite(scale)) return fail_status(BI8_ERR_SHAPE, "%s: scale = %g must be finite", fn, scale);
+    BI8_TRY(check_pitch(fn, "ldl", ldl, E));
+    BI8_TRY(check_workspace(fn, workspace, workspace_bytes));
+    if (!expert_offsets || (T > 0 && (!logits || !topk_ids || !topk_weights || !sorted_token || !row_of)))
+        return null_pointer(fn);
+    BI8_TRY(check_align(fn, "logits", logits, logits_bf16 ? 2 : 4));
+    BI8_TRY(check_align(fn, "bias", bias, 4));
+    BI8_TRY(check_align(fn, "topk_ids", topk_ids, 4));
+    BI8_TRY(check_align(fn, "topk_weights", topk_weights, 4));
+    BI8_TRY(check_align(fn, "sorted_token", sorted_token, 4));
+    BI8_TRY(check_align(fn, "expert_offsets", expert_offsets, 4));
+    BI8_TRY(check_align(fn, "row_of", row_of, 4));
+    const int64_t need = T > 0 ? bi8::route_grouped_workspace_bytes(T, E) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn,
+                           (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    bi8::RouteArgs p{};
+    p.logits = logits, p.bf16 = logits_bf16 != 0, p.ldl = ldl, p.bias = bias, p.T = T, p.E = E, p.k = k;
+    p.score = score, p.groups = groups, p.topk_groups = topk_groups, p.group_top = group_top;
+    p.renormalize = renormalize != 0, p.scale = scale;
+    p.ids = topk_ids, p.weights = topk_weights, p.sorted_token = sorted_token, p.offsets = expert_offsets;
+    p.row_of = row_of;
+    return bi8::call_status(fn, bi8::launch_moe_route_grouped(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -113,6 +113,25 @@ hipError_t launch_rmsnorm_quant(bool fp8, const uint16_t *x, int64_t ldx, const 
                                 const uint16_t *weight, double eps, int64_t M, int64_t H, uint16_t *h, int64_t ldh,
                                 uint16_t *y, void *xq, float *xs, hipStream_t stream);
 
+// Router with scores, a bias and groups (route.hip).
+struct RouteArgs {
+    const void *logits;   // [T, ldl], fp32 or bf16
+    const float *bias;    // null: none
+    int32_t *ids;
+    float *weights;
+    int32_t *sorted_token, *offsets, *row_of;
+    int64_t ldl, T;
+    double scale;
+    int32_t bf16, E, k, score, groups, topk_groups, group_top, renormalize;
+    // the launch's own: B tokens a workgroup, and on the workspace the counts
+    // [workgroup, pitch], their sums over the workgroups before, the totals
+    int32_t block_tokens, log_groups, pitch;
+    uint8_t *counts;
+    int32_t *before, *totals;
+};
+int64_t route_grouped_workspace_bytes(int64_t T, int32_t E);
+hipError_t launch_moe_route_grouped(RouteArgs p, void *workspace, hipStream_t stream);
+
 // Norm and rotation of query and key heads (heads.hip).
 constexpr int kMaxAxes = 4;
 struct HeadsArgs {

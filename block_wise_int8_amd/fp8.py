@@ -229,9 +229,11 @@ def moe_gemm_silu_quant_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: 
     return aq, as_
 
 
-def moe_layer_fp8_workspace_size(T: int, H: int, I: int, E: int, k: int) -> int:
-    """Bytes of workspace ``moe_layer_fp8`` needs for T tokens."""
-    return int(_bi8.load().blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k))
+def moe_layer_fp8_workspace_size(T: int, H: int, I: int, E: int, k: int, routed: bool = False) -> int:
+    """Bytes of workspace ``moe_layer_fp8`` needs for T tokens (``routed``: with a given ``route``)."""
+    lib = _bi8.load()
+    fn = lib.blockint8_moe_layer_fp8_routed_workspace_size if routed else lib.blockint8_moe_layer_fp8_workspace_size
+    return int(fn(T, H, I, E, k))
 
 
 def moe_layer_fp8_select(T: int, H: int, I: int, E: int, k: int) -> int:
@@ -239,9 +241,10 @@ def moe_layer_fp8_select(T: int, H: int, I: int, E: int, k: int) -> int:
     return int(_bi8.load().blockint8_moe_layer_fp8_select(T, H, I, E, k))
 
 
-def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13: torch.Tensor, w2: torch.Tensor,
-                  ws2: torch.Tensor, k: int, renormalize: bool = False, out: torch.Tensor | None = None,
-                  workspace: torch.Tensor | None = None, variant: int | None = None) -> torch.Tensor:
+def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor | None, w13: torch.Tensor, ws13: torch.Tensor,
+                  w2: torch.Tensor, ws2: torch.Tensor, k: int, renormalize: bool = False,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, variant: int | None = None,
+                  route=None) -> torch.Tensor:
     """The e4m3 FusedMoE layer on the GPU, through one C call: route, gather +
     quantise, w13 grouped GEMM (moe_layer_fp8_select), SiLU gating + quantise,
     w2 grouped GEMM, weighted combine.  Where the w13 GEMM runs 256-row weight
@@ -253,13 +256,20 @@ def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13
     ``moe_layer_fp8_workspace_size`` bytes or more (a fresh one when not
     given); calls that share one must not overlap in time.  ``variant``
     GEMM_TILE_256X128_F16 holds the w13 GEMM's sums, which the second quantiser
-    reads, whatever its size.  Returns bf16 [T, H]."""
+    reads, whatever its size.  ``route``: the five tensors of ``moe_route`` or
+    ``moe_route_grouped`` with this k (up to 32 then), in the place of the logits
+    (None then, and ``renormalize`` False).  Returns bf16 [T, H]."""
     dev = c.device_of(x, "x")
     T, H, ldx = c.rows(x, "x", dev)
-    rows, E = c.matrix(logits, "logits", dev, torch.float32)
-    if rows != T:
-        raise ValueError("logits must have %d rows (got %d)" % (T, rows))
-    c.dense(w13, "w13", dev, FP8, (E, None, H))
+    if route is None:
+        rows, E = c.matrix(logits, "logits", dev, torch.float32)
+        if rows != T:
+            raise ValueError("logits must have %d rows (got %d)" % (T, rows))
+        c.dense(w13, "w13", dev, FP8, (E, None, H))
+    else:
+        c.dense(w13, "w13", dev, FP8, (None, None, H))
+        E = w13.shape[0]
+        route = c.routing(route, x, logits, renormalize, E, k)
     N = w13.shape[1]
     if N % 2:
         raise ValueError("w13 must have an even number of rows (gate, then up)")
@@ -270,9 +280,14 @@ def moe_layer_fp8(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, ws13
     out = c.output(out, "out", dev, torch.bfloat16, (T, H))
     lib = _bi8.load()
     if workspace is None:
-        workspace = torch.empty(lib.blockint8_moe_layer_fp8_workspace_size(T, H, I, E, k), dtype=torch.uint8,
+        workspace = torch.empty(moe_layer_fp8_workspace_size(T, H, I, E, k, route is not None), dtype=torch.uint8,
                                 device=dev)
     wsp, nbytes = c.scratch(workspace, dev)
+    if route is not None:
+        _bi8._check(c.call(lib.blockint8_moe_layer_fp8_routed, dev, variant or 0, x.data_ptr(), ldx,
+                           *[t.data_ptr() for t in route], w13.data_ptr(), ws13.data_ptr(), w2.data_ptr(),
+                           ws2.data_ptr(), out.data_ptr(), T, H, I, E, k, 128, 128, wsp, nbytes))
+        return out
     _bi8._check(c.call(lib.blockint8_moe_layer_fp8_variant, dev, variant or 0, x.data_ptr(), ldx, logits.data_ptr(),
                        w13.data_ptr(), ws13.data_ptr(), w2.data_ptr(), ws2.data_ptr(), out.data_ptr(), T, H, I, E, k,
                        1 if renormalize else 0, 128, 128, wsp, nbytes))

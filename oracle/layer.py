@@ -35,3 +35,53 @@ def head_norm_rope(x, weight, eps, table, positions, sections, rot, interleaved)
             mag[t, :, a] = np.abs(u[t, :, a] * c) + np.abs(u[t, :, b] * s)
             mag[t, :, b] = np.abs(u[t, :, b] * c) + np.abs(u[t, :, a] * s)
     return out, mag
+
+
+def scores(logits, kind):
+    """Scores in binary64: softmax (rows of nothing but -infinity: zeros) or sigmoid.  NaN counts as -infinity,
+    +infinity as the largest finite binary32 value."""
+    l = np.asarray(logits, np.float64)
+    l = np.where(np.isnan(l), -np.inf, np.minimum(l, np.finfo(np.float32).max))
+    with np.errstate(over="ignore", invalid="ignore"):
+        if kind == "sigmoid":
+            return l, np.where(np.isneginf(l), 0.0, 1.0 / (1.0 + np.exp(-l)))
+        e = np.where(np.isneginf(l), 0.0, np.exp(l - l.max(axis=1, keepdims=True)))
+    total = e.sum(axis=1, keepdims=True)
+    return l, e / np.where(total > 0, total, 1.0)
+
+
+def route_grouped(logits, k, kind, bias, groups, topk_groups, group_top, renormalize, scale):
+    """(ids [T, k], weights [T, k]) by sorting each token's experts."""
+    l, p = scores(logits, kind)
+    T, E = p.shape
+    n = E // groups
+    value = p if bias is None else p + np.where(np.isnan(bias), -np.inf, bias).astype(np.float64)
+    choice = l if bias is None else value
+    ids, weights = np.zeros((T, k), np.int32), np.zeros((T, k))
+    for t in range(T):
+        kept = range(E)
+        if topk_groups < groups:
+            best = []
+            for g in range(groups):
+                members = sorted((value[t, e] if bias is not None or group_top == 2 else l[t, e]
+                                  for e in range(g * n, (g + 1) * n)), reverse=True)
+                best.append((-sum(members[:group_top]), g))
+            kept = [e for _, g in sorted(best)[:topk_groups] for e in range(g * n, (g + 1) * n)]
+        ids[t] = [e for _, e in sorted((-choice[t, e], e) for e in kept)[:k]]
+        w = p[t, ids[t]]
+        if renormalize:
+            w = w / w.sum() if w.sum() > 0 else np.zeros(k)
+        weights[t] = w * scale
+    return ids, weights
+
+
+def dispatch(ids, E):
+    """(sorted_token, expert_offsets, row_of) of the rows in the order of (expert, token, slot)."""
+    T, k = ids.shape
+    rows = sorted((int(ids[t, s]), t, s) for t in range(T) for s in range(k))
+    sorted_token = np.array([t for _, t, _ in rows], np.int32)
+    row_of = np.zeros((T, k), np.int32)
+    for r, (_, t, s) in enumerate(rows):
+        row_of[t, s] = r
+    offsets = np.searchsorted(np.array([e for e, _, _ in rows] or [E]), np.arange(E + 1)) if T * k else np.zeros(E + 1)
+    return sorted_token, offsets.astype(np.int32), row_of

@@ -25,6 +25,11 @@ CALLS = {
                          eps=1e-6, table=P, P=16, positions=P, positions_axis=0, axes=1, sections=sections(32),
                          interleaved=0, T=3, D=64, rot=64, q_out=P, qo_token=256, qo_head=64, k_out=P, ko_token=128,
                          ko_head=64),
+    "moe_route_grouped": dict(logits=P, bf16=0, ldl=64, bias=P, T=100, E=64, k=4, score=1, groups=8, topk_groups=2,
+                              group_top=2, renorm=1, scale=1.0, ids=P, weights=P, st=P, off=P, row_of=P, wsp=P,
+                              nbytes=1 << 20),
+    "moe_layer_fp8_routed": dict(variant=0, x=P, ldx=256, weights=P, st=P, off=P, row_of=P, w13=P, ws13=P, w2=P, ws2=P,
+                                 out=P, T=4, H=256, I=256, E=16, k=9, bn=128, bk=128, wsp=P, nbytes=1 << 30),
 }
 
 BAD = {
@@ -43,7 +48,27 @@ BAD = {
         (dict(qo_token=64, qo_head=191), SHAPE), (dict(qo_token=64, qo_head=128), SHAPE),
         (dict(q=ODD), ALIGN), (dict(k=ODD), ALIGN), (dict(q_weight=ODD), ALIGN), (dict(k_weight=ODD), ALIGN),
         (dict(table=P + 2), ALIGN), (dict(positions=P + 2), ALIGN), (dict(q_out=ODD), ALIGN), (dict(k_out=ODD), ALIGN)],
+    "moe_route_grouped": [(dict([(name, None)]), NULL) for name in ("logits", "ids", "weights", "st", "off", "row_of")] + [
+        (dict(T=-1), SHAPE), (dict(T=1 << 29), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(k=0), SHAPE),
+        (dict(k=33), SHAPE), (dict(E=8, k=9), SHAPE), (dict(ldl=63), SHAPE), (dict(score=2), SHAPE), (dict(score=-1), SHAPE),
+        (dict(groups=0), SHAPE), (dict(groups=7), SHAPE), (dict(groups=128, E=128), SHAPE), (dict(topk_groups=0), SHAPE),
+        (dict(topk_groups=9), SHAPE), (dict(k=17), SHAPE), (dict(groups=64, topk_groups=3), SHAPE), (dict(group_top=0), SHAPE),
+        (dict(group_top=3), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE),
+        (dict(wsp=None), SHAPE), (dict(nbytes=7 * 64 - 1), SHAPE), (dict(nbytes=-1), SHAPE), (dict(logits=P + 2), ALIGN),
+        (dict(logits=ODD, bf16=1), ALIGN), (dict(bias=P + 2), ALIGN), (dict(ids=P + 2), ALIGN), (dict(weights=P + 1), ALIGN),
+        (dict(st=P + 2), ALIGN), (dict(off=P + 2), ALIGN), (dict(row_of=P + 2), ALIGN), (dict(wsp=P + 8), ALIGN)],
+    "moe_layer_fp8_routed": [(dict([(name, None)]), NULL) for name in ("x", "weights", "st", "off", "row_of", "w13", "ws13",
+                                                                     "w2", "ws2", "out", "wsp")] + [
+        (dict(variant=1), SHAPE), (dict(variant=-1), SHAPE), (dict(T=-1), SHAPE), (dict(T=1 << 30), SHAPE), (dict(H=0), SHAPE),
+        (dict(I=0), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=17), SHAPE),
+        (dict(E=64, k=33), SHAPE), (dict(ldx=255), SHAPE), (dict(nbytes=0), SHAPE), (dict(nbytes=4096), SHAPE), (dict(H=248), ALIGN),
+        (dict(I=40), ALIGN), (dict(bn=64), BLOCK), (dict(bk=1), BLOCK), (dict(x=ODD), ALIGN), (dict(weights=P + 2), ALIGN),
+        (dict(st=P + 2), ALIGN), (dict(off=P + 2), ALIGN), (dict(row_of=P + 2), ALIGN), (dict(w13=P + 8), ALIGN),
+        (dict(ws13=P + 2), ALIGN), (dict(w2=P + 8), ALIGN), (dict(ws2=P + 2), ALIGN), (dict(out=P + 8), ALIGN),
+        (dict(wsp=P + 128), ALIGN)],
 }
+# calls that write something even without tokens
+NOT_EMPTY = {"moe_route_grouped"}
 
 
 def run(name, **kw):
@@ -58,7 +83,7 @@ def test_refusals(name, kw, status):
     assert bi8.load().blockint8_last_error().decode().startswith("blockint8_" + name + ":")
 
 
-@pytest.mark.parametrize("name", sorted(CALLS))
+@pytest.mark.parametrize("name", sorted(set(CALLS) - NOT_EMPTY))
 def test_empty_is_a_no_op(name):
     size = next(k for k in ("M", "R", "N", "T") if k in CALLS[name])
     none = {k: None for k, v in CALLS[name].items() if v == P}
@@ -66,7 +91,7 @@ def test_empty_is_a_no_op(name):
     assert bi8.load().blockint8_last_error().decode() == ""
 
 
-@pytest.mark.parametrize("header", ["blockint8_heads.h"])
+@pytest.mark.parametrize("header", ["blockint8_heads.h", "blockint8_route.h"])
 def test_every_declared_function_is_exported(header):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", header)).read(), flags=re.S)
     names = set(re.findall(r"\b(blockint8_\w+)\s*\(", text))
@@ -78,6 +103,17 @@ def test_every_declared_function_is_exported(header):
 
 def test_binding_has_no_cpu_path():
     x = torch.zeros(4, 2, 8, dtype=torch.bfloat16)
-    for fn in (lambda: bi8.qk_norm_rope(x, x, torch.zeros(4, dtype=torch.int32), torch.zeros(4, 8)),):
+    for fn in (lambda: bi8.qk_norm_rope(x, x, torch.zeros(4, dtype=torch.int32), torch.zeros(4, 8)),
+               lambda: bi8.moe_route_grouped(torch.zeros(4, 8), 2)):
         with pytest.raises(ValueError, match="HIP device"):
             fn()
+
+
+def test_workspace_sizes():
+    size = bi8.moe_route_grouped_workspace_size
+    assert size(0, 64) == size(-1, 64) == size(100, 0) == size(100, 1025) == size(1 << 31, 64) == size(16, 64) == 0
+    assert size(17, 64) > 0 and size(100, 64) == 7 * 64 and size(1 << 20, 1024) > (1 << 14) * 1024 * 5
+    routed = bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 9, routed=True)
+    assert routed > 0 and bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 9) == 0
+    assert bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 33, routed=True) == 0
+    assert bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 2, True) < bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 2)

@@ -57,3 +57,45 @@ def test_positions_outside_the_table():
     x = np.ones((3, 1, 4))
     out = layer.head_norm_rope(x, None, 0.0, table(4, 4), np.array([[-1, 4, 3]]), [2], 4, False)[0]
     assert np.isnan(out[:2]).all() and np.isfinite(out[2]).all()
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_softmax_routing_is_the_plain_router(renormalize):
+    import oracle
+
+    rng = np.random.default_rng(5)
+    logits = rng.standard_normal((40, 12)).astype(np.float32)
+    ids, w = layer.route_grouped(logits, 3, "softmax", None, 1, 1, 1, renormalize, 1.0)
+    ids0, w0 = oracle.topk_softmax(logits, 3, renormalize)
+    assert np.array_equal(ids, ids0) and np.allclose(w, w0, rtol=1e-6)
+    st, off, row_of = layer.dispatch(ids, 12)
+    st0, off0, row0 = oracle.moe_align(ids0, 12)
+    assert np.array_equal(st, st0) and np.array_equal(off, off0) and np.array_equal(row_of, row0)
+
+
+def test_groups_and_bias_by_hand():
+    # scores of the sigmoid: 0 -> 0.5, large -> 1
+    l = np.array([[0, 0, 9, -9, 1, 1, -1, 2]], np.float32)   # groups (0 0) (9 -9) (1 1) (-1 2)
+    args = dict(kind="sigmoid", groups=4, renormalize=False, scale=2.0)
+    ids, w = layer.route_grouped(l, 2, bias=None, topk_groups=1, group_top=1, **args)
+    assert ids.tolist() == [[2, 3]] and np.allclose(w, 2 / (1 + np.exp([[-9.0, 9.0]])))
+    ids, _ = layer.route_grouped(l, 2, bias=None, topk_groups=1, group_top=2, **args)
+    assert ids.tolist() == [[4, 5]]
+    bias = np.array([0.9, 0.8, 0, 0, 0, 0, 0, 0])
+    ids, w = layer.route_grouped(l, 3, bias=bias, topk_groups=2, group_top=2, **args)
+    assert ids.tolist() == [[0, 1, 4]] and np.allclose(w[0, :2], 1.0)   # the bias is not in the weights
+    bias = np.array([0, 0, 0, 0, -np.inf, 0, 0, np.nan])
+    ids, _ = layer.route_grouped(l, 8, bias=bias, topk_groups=4, group_top=2, **args)
+    assert ids.tolist() == [[2, 5, 0, 1, 6, 3, 4, 7]]
+
+
+def test_rows_of_nothing():
+    l = np.full((2, 4), -np.inf)
+    l[1, 2] = np.nan
+    for kind in ("softmax", "sigmoid"):
+        for renormalize in (False, True):
+            ids, w = layer.route_grouped(l, 2, kind, None, 1, 1, 1, renormalize, 1.0)
+            assert ids.tolist() == [[0, 1], [0, 1]] and not w.any()
+    l[0, 3] = l[0, 1] = np.inf
+    ids, w = layer.route_grouped(l, 2, "softmax", None, 1, 1, 1, False, 1.0)
+    assert ids[0].tolist() == [1, 3] and w[0].tolist() == [0.5, 0.5]
