@@ -18,6 +18,7 @@ Entry points (same names as the C ABI, without the ``blockint8_`` prefix):
   and :func:`moe_layer`, the whole FusedMoE layer built from them
 * :func:`rmsnorm_quant` -- residual addition, RMS norm and quantisation (int8
   or e4m3 codes), what feeds the linears and the MoE layer
+* :func:`lora_add` -- low-rank adapters of many requests beside a shared projection
 * :func:`moe_route_grouped` -- the router with softmax or sigmoid scores, a bias
   for balance and groups of experts; the MoE layers take its result as ``route``
 * :func:`qk_norm_rope` -- norm of query and key heads and their rotation by
@@ -116,6 +117,7 @@ def load() -> ctypes.CDLL:
     fp8.declare(lib)
     norm.declare(lib)
     heads.declare(lib)
+    lora.declare(lib)
     _route.declare(lib)
     _lib = lib
     return lib
@@ -595,10 +597,11 @@ def check_tp_partition(input_size: int, input_size_per_partition: int, output_pa
                                                len(output_partition_sizes), int(tp_size), block[0], block[1]))
 
 
-from . import _call, fp8, heads, norm, route as _route  # noqa: E402  (they use the names above)
+from . import _call, fp8, heads, lora, norm, route as _route  # noqa: E402  (they use the names above)
 from .fp8 import *  # noqa: E402,F401,F403
 from .heads import *  # noqa: E402,F401,F403
+from .lora import *  # noqa: E402,F401,F403
 from .norm import *  # noqa: E402,F401,F403
 from .route import *  # noqa: E402,F401,F403
 
-__all__ += fp8.__all__ + norm.__all__ + heads.__all__ + _route.__all__
+__all__ += fp8.__all__ + norm.__all__ + heads.__all__ + lora.__all__ + _route.__all__

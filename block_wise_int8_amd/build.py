@@ -26,7 +26,7 @@ CLOCK_LIB_PATH = os.path.join(PKG, "libbi8clock.so")
 
 SOURCES = ["abi.cpp", "quant_act.hip", "gemm.hip", "moe.hip", "noalloc.hip",
            "abi_fp8.cpp", "quant_fp8.hip", "gemm_fp8.hip", "norm.hip",
-           "abi_layer.cpp", "heads.hip", "route.hip"]
+           "abi_layer.cpp", "heads.hip", "route.hip", "lora.hip"]
 CLOCK_SOURCES = ["clockprobe.hip"]
 ARCH = "gfx950"
 

@@ -1,6 +1,6 @@
 // C ABI of the operators beside the 8-bit products: argument checks on the host,
-// then the launches on the caller's stream.  See include/blockint8_heads.h and
-// include/blockint8_route.h for the contracts.
+// then the launches on the caller's stream.  See include/blockint8_heads.h,
+// include/blockint8_route.h and include/blockint8_lora.h for the contracts.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "../../include/blockint8_heads.h"
+#include "../../include/blockint8_lora.h"
 #include "../../include/blockint8_route.h"
 #include "checks.hpp"
 #include "internal.hpp"
@@ -152,6 +153,60 @@ int32_t blockint8_moe_route_grouped(const void *logits, int32_t logits_bf16, int
     p.ids = topk_ids, p.weights = topk_weights, p.sorted_token = sorted_token, p.offsets = expert_offsets;
     p.row_of = row_of;
     return bi8::call_status(fn, bi8::launch_moe_route_grouped(p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int64_t blockint8_lora_add_workspace_size(int64_t M, int64_t K, int32_t R, int32_t parts) {
+    if (M <= 0 || M > kMaxRows || K <= 0 || K > BI8_MAX_K || R < 8 || R % 8 != 0 || parts < 1 ||
+        parts > BI8_MAX_PARTS || R > BI8_MAX_RANKS / parts)
+        return 0;
+    return bi8::lora_workspace_bytes(M, K, parts * R);
+}
+
+int32_t blockint8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b, const float *scales,
+                           const int32_t *adapter, uint16_t *y, int64_t ldy, int64_t M, int64_t N, int64_t K, int32_t L,
+                           int32_t R, int32_t parts, const int64_t *part_columns, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+    static const char fn[] = "blockint8_lora_add";
+    static_assert(BI8_MAX_PARTS == bi8::kMaxParts, "parts");
+    BI8_TRY(check_rows(fn, "M", M));
+    if (N <= 0 || N > kMaxRows) return fail_status(BI8_ERR_SHAPE, "%s: N = %lld out of range", fn, (long long)N);
+    BI8_TRY(check_columns(fn, "K", K));
+    if (L < 1 || L > 1 << 24) return fail_status(BI8_ERR_SHAPE, "%s: L = %d out of range [1, 2^24]", fn, L);
+    if (parts < 1 || parts > BI8_MAX_PARTS)
+        return fail_status(BI8_ERR_SHAPE, "%s: parts = %d out of range [1, %d]", fn, parts, BI8_MAX_PARTS);
+    if (R < 1 || R > BI8_MAX_RANKS / parts)
+        return fail_status(BI8_ERR_SHAPE, "%s: R = %d out of range [1, %d] for %d parts", fn, R, BI8_MAX_RANKS / parts,
+                           parts);
+    if (R % 8 != 0) return fail_status(BI8_ERR_ALIGN, "%s: R = %d must be a multiple of 8", fn, R);
+    if (!part_columns) return null_pointer(fn);
+    int64_t columns = 0;
+    for (int32_t i = 0; i < parts; ++i) {
+        if (part_columns[i] < 1 || part_columns[i] > N)
+            return fail_status(BI8_ERR_SHAPE, "%s: part %d has %lld columns", fn, i, (long long)part_columns[i]);
+        columns += part_columns[i];
+    }
+    if (columns != N)
+        return fail_status(BI8_ERR_SHAPE, "%s: the parts have %lld columns, not %lld", fn, (long long)columns,
+                           (long long)N);
+    BI8_TRY(check_pitch(fn, "ldx", ldx, K));
+    BI8_TRY(check_pitch(fn, "ldy", ldy, N));
+    BI8_TRY(check_workspace(fn, workspace, workspace_bytes));
+    if (M == 0) return done(fn);
+    if (!x || !a || !b || !adapter || !y || !workspace) return null_pointer(fn);
+    BI8_TRY(check_align(fn, "x", x, 2));
+    BI8_TRY(check_align(fn, "a", a, 16));
+    BI8_TRY(check_align(fn, "b", b, 16));
+    BI8_TRY(check_align(fn, "scales", scales, 4));
+    BI8_TRY(check_align(fn, "adapter", adapter, 4));
+    BI8_TRY(check_align(fn, "y", y, 2));
+    const int64_t need = bi8::lora_workspace_bytes(M, K, parts * R);
+    if (workspace_bytes < need)
+        return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
+                           (long long)need);
+    bi8::LoraArgs p{};
+    p.x = x, p.ldx = ldx, p.a = a, p.b = b, p.scales = scales, p.adapter = adapter, p.y = y, p.ldy = ldy;
+    p.M = M, p.N = N, p.K = K, p.L = L, p.R = R, p.ranks = parts * R, p.t = static_cast<float *>(workspace);
+    return bi8::call_status(fn, bi8::launch_lora_add(p, part_columns, parts, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

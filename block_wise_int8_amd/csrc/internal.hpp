@@ -132,6 +132,27 @@ struct RouteArgs {
 int64_t route_grouped_workspace_bytes(int64_t T, int32_t E);
 hipError_t launch_moe_route_grouped(RouteArgs p, void *workspace, hipStream_t stream);
 
+// Low-rank adapters beside a projection (lora.hip).
+constexpr int kMaxParts = 4;
+struct LoraArgs {
+    const uint16_t *x, *a, *b;   // [M, ldx], [L, ranks, K], [L, N, R]
+    const float *scales;         // null: 1
+    const int32_t *adapter;
+    uint16_t *y;
+    float *t;                    // [splits, M, ranks]
+    int64_t ldx, ldy, M, N, K;
+    int32_t L, R, ranks;
+    // the launch's own: columns of K a wave, of y a workgroup; workgroups that
+    // share the rows of a block; first column and block of columns of each part,
+    // and behind the last
+    int32_t splits, slots, columns;
+    int64_t slice;
+    int64_t part_first[kMaxParts + 1];
+    int32_t part_blocks[kMaxParts + 1];
+};
+int64_t lora_workspace_bytes(int64_t M, int64_t K, int32_t ranks);
+hipError_t launch_lora_add(LoraArgs p, const int64_t *part_columns, int32_t parts, hipStream_t stream);
+
 // Norm and rotation of query and key heads (heads.hip).
 constexpr int kMaxAxes = 4;
 struct HeadsArgs {

@@ -85,3 +85,24 @@ def dispatch(ids, E):
         row_of[t, s] = r
     offsets = np.searchsorted(np.array([e for e, _, _ in rows] or [E]), np.arange(E + 1)) if T * k else np.zeros(E + 1)
     return sorted_token, offsets.astype(np.int32), row_of
+
+
+def lora_add(y, x, a, b, scales, adapter, parts):
+    """y [M, N], x [M, K], a [L, P R, K], b [L, N, R] -> (the result, what its rounding errors are relative to).
+
+    The second: [M, N] sums of |t b| and, with |x| |a| in the place of t, of the products that made t."""
+    y, M = np.array(y, np.float64), len(adapter)
+    of_t, of_x = np.zeros_like(y), np.zeros_like(y)
+    R, first = b.shape[2], np.concatenate([[0], np.cumsum(parts)])
+    for m in range(M):
+        e = adapter[m]
+        if not 0 <= e < len(a):
+            continue
+        s = 1.0 if scales is None else float(scales[e])
+        t, tx = s * (a[e] @ x[m]), abs(s) * (np.abs(a[e]) @ np.abs(x[m]))
+        for p in range(len(parts)):
+            cols, ranks = slice(first[p], first[p + 1]), slice(p * R, (p + 1) * R)
+            y[m, cols] += b[e, cols] @ t[ranks]
+            of_t[m, cols] = np.abs(b[e, cols]) @ np.abs(t[ranks])
+            of_x[m, cols] = np.abs(b[e, cols]) @ tx[ranks]
+    return y, of_t, of_x

@@ -19,12 +19,18 @@ def sections(*n):
     return (ctypes.c_int32 * len(n))(*n)
 
 
+def widths(*n):
+    return (ctypes.c_int64 * len(n))(*n)
+
+
 # name -> default arguments that only the pointers' being fake makes invalid to run
 CALLS = {
     "qk_norm_rope": dict(q=P, q_token=384, q_head=64, Hq=4, k=P, k_token=384, k_head=64, Hk=2, q_weight=P, k_weight=P,
                          eps=1e-6, table=P, P=16, positions=P, positions_axis=0, axes=1, sections=sections(32),
                          interleaved=0, T=3, D=64, rot=64, q_out=P, qo_token=256, qo_head=64, k_out=P, ko_token=128,
                          ko_head=64),
+    "lora_add": dict(x=P, ldx=64, a=P, b=P, scales=P, adapter=P, y=P, ldy=96, M=5, N=96, K=64, L=3, R=16, parts=2,
+                     widths=widths(64, 32), wsp=P, nbytes=1 << 20),
     "moe_route_grouped": dict(logits=P, bf16=0, ldl=64, bias=P, T=100, E=64, k=4, score=1, groups=8, topk_groups=2,
                               group_top=2, renorm=1, scale=1.0, ids=P, weights=P, st=P, off=P, row_of=P, wsp=P,
                               nbytes=1 << 20),
@@ -48,6 +54,14 @@ BAD = {
         (dict(qo_token=64, qo_head=191), SHAPE), (dict(qo_token=64, qo_head=128), SHAPE),
         (dict(q=ODD), ALIGN), (dict(k=ODD), ALIGN), (dict(q_weight=ODD), ALIGN), (dict(k_weight=ODD), ALIGN),
         (dict(table=P + 2), ALIGN), (dict(positions=P + 2), ALIGN), (dict(q_out=ODD), ALIGN), (dict(k_out=ODD), ALIGN)],
+    "lora_add": [(dict([(name, None)]), NULL) for name in ("x", "a", "b", "adapter", "y", "widths", "wsp")] + [
+        (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=0), SHAPE), (dict(N=1 << 31), SHAPE), (dict(K=0), SHAPE),
+        (dict(K=1 << 24, ldx=1 << 24), SHAPE), (dict(L=0), SHAPE), (dict(L=(1 << 24) + 1), SHAPE), (dict(R=0), SHAPE),
+        (dict(R=136), SHAPE), (dict(R=-8), SHAPE), (dict(parts=0), SHAPE), (dict(parts=5), SHAPE),
+        (dict(widths=widths(64, 31)), SHAPE), (dict(widths=widths(96, 0)), SHAPE), (dict(widths=widths(97, -1)), SHAPE),
+        (dict(ldx=63), SHAPE), (dict(ldy=95), SHAPE), (dict(nbytes=5 * 32 * 4 - 1), SHAPE), (dict(nbytes=-1), SHAPE),
+        (dict(R=12), ALIGN), (dict(x=ODD), ALIGN), (dict(a=P + 8), ALIGN), (dict(b=P + 2), ALIGN),
+        (dict(scales=P + 2), ALIGN), (dict(adapter=P + 1), ALIGN), (dict(y=ODD), ALIGN), (dict(wsp=P + 8), ALIGN)],
     "moe_route_grouped": [(dict([(name, None)]), NULL) for name in ("logits", "ids", "weights", "st", "off", "row_of")] + [
         (dict(T=-1), SHAPE), (dict(T=1 << 29), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(k=0), SHAPE),
         (dict(k=33), SHAPE), (dict(E=8, k=9), SHAPE), (dict(ldl=63), SHAPE), (dict(score=2), SHAPE), (dict(score=-1), SHAPE),
@@ -91,7 +105,7 @@ def test_empty_is_a_no_op(name):
     assert bi8.load().blockint8_last_error().decode() == ""
 
 
-@pytest.mark.parametrize("header", ["blockint8_heads.h", "blockint8_route.h"])
+@pytest.mark.parametrize("header", ["blockint8_heads.h", "blockint8_route.h", "blockint8_lora.h"])
 def test_every_declared_function_is_exported(header):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", header)).read(), flags=re.S)
     names = set(re.findall(r"\b(blockint8_\w+)\s*\(", text))
@@ -104,7 +118,8 @@ def test_every_declared_function_is_exported(header):
 def test_binding_has_no_cpu_path():
     x = torch.zeros(4, 2, 8, dtype=torch.bfloat16)
     for fn in (lambda: bi8.qk_norm_rope(x, x, torch.zeros(4, dtype=torch.int32), torch.zeros(4, 8)),
-               lambda: bi8.moe_route_grouped(torch.zeros(4, 8), 2)):
+               lambda: bi8.moe_route_grouped(torch.zeros(4, 8), 2),
+               lambda: bi8.lora_add(x[0], x[0], x, x, torch.zeros(2, dtype=torch.int32))):
         with pytest.raises(ValueError, match="HIP device"):
             fn()
 
@@ -117,3 +132,7 @@ def test_workspace_sizes():
     assert routed > 0 and bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 9) == 0
     assert bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 33, routed=True) == 0
     assert bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 2, True) < bi8.moe_layer_fp8_workspace_size(4, 256, 256, 16, 2)
+    size = bi8.lora_add_workspace_size
+    assert size(0, 64, 8) == size(-1, 64, 8) == size(5, 0, 8) == size(5, 64, 12) == size(5, 64, 264) == 0
+    assert size(5, 64, 136, 2) == size(5, 64, 8, 0) == size(5, 64, 8, 5) == size(1 << 31, 64, 8) == 0
+    assert size(5, 64, 16, 2) == 5 * 32 * 4 and size(1, 4096, 16) % (16 * 4) == 0

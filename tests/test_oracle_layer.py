@@ -99,3 +99,21 @@ def test_rows_of_nothing():
     l[0, 3] = l[0, 1] = np.inf
     ids, w = layer.route_grouped(l, 2, "softmax", None, 1, 1, 1, False, 1.0)
     assert ids[0].tolist() == [1, 3] and w[0].tolist() == [0.5, 0.5]
+
+
+def test_adapters_are_a_change_of_the_weight():
+    rng = np.random.default_rng(6)
+    M, N, K, L, R = 6, 10, 7, 3, 2
+    x, y, a, b = (rng.standard_normal(s) for s in ((M, K), (M, N), (L, 2 * R, K), (L, N, R)))
+    s, adapter = np.array([0.5, 2.0, -1.0]), np.array([2, 0, -1, 1, 3, 2])
+    out, of_t, of_x = layer.lora_add(y, x, a, b, s, adapter, [4, 6])
+    for m in range(M):
+        e = adapter[m]
+        if not 0 <= e < L:
+            assert np.array_equal(out[m], y[m]) and not of_t[m].any()
+            continue
+        change = s[e] * np.concatenate([b[e, :4] @ a[e, :R], b[e, 4:] @ a[e, R:]])
+        assert np.allclose(out[m], y[m] + change @ x[m])
+        assert np.all(of_x[m] >= of_t[m] - 1e-12) and np.all(of_t[m] >= np.abs(out[m] - y[m]) - 1e-12)
+    assert np.allclose(layer.lora_add(y, x, a, b, None, adapter, [4, 6])[0][1], layer.lora_add(
+        y, x, a, b, np.ones(3), adapter, [4, 6])[0][1])
