@@ -166,7 +166,10 @@ struct HeadsArgs {
     double eps;
     int32_t Hq, Hk, D, rot, axes, interleaved;
     int32_t first[kMaxAxes];           // first pair of each axis (unused axes: past every pair)
-    int32_t log_lanes, share, table_chunks;   // the launch's own
+    // the launch's own: lanes a head, groups of lanes a token and heads of each at
+    // most, whether a chunk of pairs is one piece of the table, 1 / D
+    int32_t log_lanes, q_groups, k_groups, each, table_chunks;
+    double inverse;
 };
 hipError_t launch_qk_norm_rope(HeadsArgs p, hipStream_t stream);
 

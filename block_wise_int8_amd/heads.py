@@ -20,17 +20,25 @@ def declare(lib) -> None:
 
 def _heads(t, name: str, dev: int, T=None, H=None, D=None):
     """Check bf16 [tokens, heads, values] with contiguous values: its shape and strides."""
+    try:
+        if t.dtype is torch.bfloat16 and t.get_device() == dev:
+            n, h, d = t.shape
+            token, head, step = t.stride()
+            if step == 1 and (T is None or (n == T and d == D and (H is None or h == H))):
+                return n, h, d, token, head
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise TypeError("%s must be a bfloat16 tensor [tokens, heads, values]" % name)
     if t.get_device() != dev:
         raise ValueError("%s must be on cuda:%d (got %s)" % (name, dev, t.device))
-    shape = t.shape
-    if any(want is not None and want != n for want, n in zip((T, H, D), shape)):
+    n, h, d = shape = t.shape
+    if any(want is not None and want != got for want, got in zip((T, H, D), shape)):
         raise ValueError("%s must have shape %s (got %s)" % (name, (T, H, D), tuple(shape)))
     token, head, step = t.stride()
-    if step != 1 and shape[2] > 1:
+    if step != 1 and d > 1:
         raise ValueError("%s must have contiguous heads (stride(2) == 1)" % name)
-    return shape, token, head
+    return n, h, d, token, head
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor,
@@ -51,10 +59,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     or the given ones, which may be ``q`` and ``k`` themselves.  A token with a
     position outside [0, P) is left out: its outputs are not written."""
     dev = c.device_of(q, "q")
-    (T, Hq, D), q_token, q_head = _heads(q, "q", dev)
+    T, Hq, D, q_token, q_head = _heads(q, "q", dev)
     Hk = k_token = k_head = k_out_token = k_out_head = 0
     if k is not None:
-        (_, Hk, _), k_token, k_head = _heads(k, "k", dev, T, None, D)
+        _, Hk, _, k_token, k_head = _heads(k, "k", dev, T, None, D)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight belong to k: there is none")
     P, rot = c.matrix(table, "table", dev, torch.float32)
@@ -77,11 +85,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
         raise ValueError("%d sections for positions of %d axes" % (len(sections), axes))
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    _, q_out_token, q_out_head = _heads(q_out, "q_out", dev, T, Hq, D)
+    *_, q_out_token, q_out_head = _heads(q_out, "q_out", dev, T, Hq, D)
     if k is not None:
         if k_out is None:
             k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev)
-        _, k_out_token, k_out_head = _heads(k_out, "k_out", dev, T, Hk, D)
+        *_, k_out_token, k_out_head = _heads(k_out, "k_out", dev, T, Hk, D)
     _bi8._check(c.call(_bi8.load().blockint8_qk_norm_rope, dev, q.data_ptr(), q_token, q_head, Hq, c.ptr(k), k_token,
                        k_head, Hk, c.ptr(q_weight), c.ptr(k_weight), eps, table.data_ptr(), P, positions.data_ptr(),
                        positions.stride(0) if axes > 1 else 0, axes, (ctypes.c_int32 * axes)(*sections),
