@@ -169,7 +169,8 @@ int32_t blockint8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     static const char fn[] = "blockint8_lora_add";
     static_assert(BI8_MAX_PARTS == bi8::kMaxParts, "parts");
     BI8_TRY(check_rows(fn, "M", M));
-    if (N <= 0 || N > kMaxRows) return fail_status(BI8_ERR_SHAPE, "%s: N = %lld out of range", fn, (long long)N);
+    if (N <= 0 || N > BI8_MAX_K)
+        return fail_status(BI8_ERR_SHAPE, "%s: N = %lld out of range [1, 2^23]", fn, (long long)N);
     BI8_TRY(check_columns(fn, "K", K));
     if (L < 1 || L > 1 << 24) return fail_status(BI8_ERR_SHAPE, "%s: L = %d out of range [1, 2^24]", fn, L);
     if (parts < 1 || parts > BI8_MAX_PARTS)
@@ -190,6 +191,8 @@ int32_t blockint8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
                            (long long)N);
     BI8_TRY(check_pitch(fn, "ldx", ldx, K));
     BI8_TRY(check_pitch(fn, "ldy", ldy, N));
+    if (ldx > BI8_MAX_K || ldy > BI8_MAX_K)
+        return fail_status(BI8_ERR_SHAPE, "%s: ldx = %lld or ldy = %lld above 2^23", fn, (long long)ldx, (long long)ldy);
     BI8_TRY(check_workspace(fn, workspace, workspace_bytes));
     if (M == 0) return done(fn);
     if (!x || !a || !b || !adapter || !y || !workspace) return null_pointer(fn);

@@ -142,10 +142,11 @@ struct LoraArgs {
     float *t;                    // [splits, M, ranks]
     int64_t ldx, ldy, M, N, K;
     int32_t L, R, ranks;
-    // the launch's own: columns of K a wave, of y a workgroup; workgroups that
-    // share the rows of a block; first column and block of columns of each part,
-    // and behind the last
-    int32_t splits, slots, columns;
+    // the launch's own: workgroups that share K, waves of one that share the ranks;
+    // workgroups that share the candidates (adapters, or rows) of a block of rows;
+    // columns of y a workgroup, of K a wave; first column and block of columns of
+    // each part, and behind the last
+    int32_t splits, rank_waves, slots, candidates, by_adapter, columns;
     int64_t slice;
     int64_t part_first[kMaxParts + 1];
     int32_t part_blocks[kMaxParts + 1];

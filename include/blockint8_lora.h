@@ -16,7 +16,6 @@ extern "C" {
 /* Parts of a projection, and the largest rank of an adapter over all its parts. */
 #define BI8_MAX_PARTS 4
 #define BI8_MAX_RANKS 256
-
 /*
  * y += s (x A^T) B^T, row by row with the row's adapter, in two launches.  The
  * projection may be several side by side (query, key and value; gate and up):
@@ -49,7 +48,7 @@ extern "C" {
  * the other).  x and y may not overlap.
  *
  * Errors: NULL pointer (M > 0; scales may be) -> BI8_ERR_NULL; M < 0, N, K, L, R
- * or parts < 1, K > BI8_MAX_K, N > 2^31 - 1, L > 2^24, parts > BI8_MAX_PARTS,
+ * or parts < 1, K, N, ldx or ldy > BI8_MAX_K, L > 2^24, parts > BI8_MAX_PARTS,
  * parts * R > BI8_MAX_RANKS, a width < 1 or another sum than N, ldx < K, ldy < N,
  * a workspace too small -> BI8_ERR_SHAPE; R % 8 != 0, a, b or workspace not
  * 16-byte, x or y not 2-byte, scales or adapter not 4-byte aligned ->

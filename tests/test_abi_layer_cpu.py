@@ -56,7 +56,8 @@ BAD = {
         (dict(table=P + 2), ALIGN), (dict(positions=P + 2), ALIGN), (dict(q_out=ODD), ALIGN), (dict(k_out=ODD), ALIGN)],
     "lora_add": [(dict([(name, None)]), NULL) for name in ("x", "a", "b", "adapter", "y", "widths", "wsp")] + [
         (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=0), SHAPE), (dict(N=1 << 31), SHAPE), (dict(K=0), SHAPE),
-        (dict(K=1 << 24, ldx=1 << 24), SHAPE), (dict(L=0), SHAPE), (dict(L=(1 << 24) + 1), SHAPE), (dict(R=0), SHAPE),
+        (dict(K=1 << 24, ldx=1 << 24), SHAPE), (dict(ldx=(1 << 23) + 1), SHAPE), (dict(ldy=(1 << 23) + 1), SHAPE),
+        (dict(N=(1 << 23) + 1, ldy=1 << 25, widths=widths(1 << 23, 1)), SHAPE), (dict(L=0), SHAPE), (dict(L=(1 << 24) + 1), SHAPE), (dict(R=0), SHAPE),
         (dict(R=136), SHAPE), (dict(R=-8), SHAPE), (dict(parts=0), SHAPE), (dict(parts=5), SHAPE),
         (dict(widths=widths(64, 31)), SHAPE), (dict(widths=widths(96, 0)), SHAPE), (dict(widths=widths(97, -1)), SHAPE),
         (dict(ldx=63), SHAPE), (dict(ldy=95), SHAPE), (dict(nbytes=5 * 32 * 4 - 1), SHAPE), (dict(nbytes=-1), SHAPE),
