@@ -76,6 +76,28 @@ __device__ __forceinline__ int32_t quant_code(float x, float s, float r) {
     return (int32_t)q;
 }
 
+// a or b, as values: between two arguments of a kernel or two members behind
+// references the conditional operator is a choice of addresses, and a load from
+// memory.
+template <class T>
+__device__ __forceinline__ T pick(bool first, T a, T b) {
+    return first ? a : b;
+}
+
+// Inclusive prefix sum over the 64 lanes by DPP: shifts right by 1, 2, 4, 8
+// within each row of 16 lanes (lanes shifted in from outside the row add 0),
+// then lane 15 of rows 0 and 2 added to rows 1 and 3, then lane 31 to rows 2
+// and 3.
+__device__ __forceinline__ int32_t wave_incl_scan(int32_t x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);   // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);   // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);   // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);   // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31
+    return x;
+}
+
 // v from the lane n places lower in its row of 16 lanes, cyclically (DPP
 // row_ror:n, a register-to-register move; n in 1..15).
 template <int N>

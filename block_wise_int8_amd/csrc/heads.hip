@@ -102,13 +102,6 @@ __device__ __forceinline__ void unit_columns(const HeadsArgs &p, int u, int &c0,
     }
 }
 
-// a or b, as values: between two arguments of a kernel the conditional operator is a
-// choice of addresses, and a load from memory.
-template <class T>
-__device__ __forceinline__ T pick(bool first, T a, T b) {
-    return first ? a : b;
-}
-
 // LP: units a lane.  A token has p.q_groups groups of lanes for its query heads
 // and p.k_groups for its key heads; group w of n takes the heads w, w + n, ...,
 // p.each at most.  FULL: every lane has two whole chunks and turns them.  NORM:

@@ -125,7 +125,8 @@ struct RouteArgs {
     int32_t bf16, E, k, score, groups, topk_groups, group_top, renormalize;
     // the launch's own: B tokens a workgroup, and on the workspace the counts
     // [workgroup, pitch], their sums over the workgroups before, the totals
-    int32_t block_tokens, log_groups, pitch;
+    // (fours: lanes load their logits four at a time)
+    int32_t block_tokens, log_groups, pitch, fours;
     uint8_t *counts;
     int32_t *before, *totals;
 };

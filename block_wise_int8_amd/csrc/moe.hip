@@ -92,20 +92,6 @@ __global__ __launch_bounds__(256) void moe_topk_kernel(const float *__restrict__
 // writes offsets[E].
 constexpr int kAlignWaves = kAlignThreads / 64;
 
-// Inclusive prefix sum over the 64 lanes by DPP: shifts right by 1, 2, 4, 8
-// within each row of 16 lanes (lanes shifted in from outside the row add 0),
-// then lane 15 of rows 0 and 2 added to rows 1 and 3, then lane 31 to rows 2
-// and 3.
-__device__ __forceinline__ int32_t wave_incl_scan(int32_t x) {
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);   // row_shr:1
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);   // row_shr:2
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);   // row_shr:4
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);   // row_shr:8
-    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15
-    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31
-    return x;
-}
-
 // Block-wide exclusive prefix (thread order) and total of x.  Two barriers;
 // wsum is reused.
 __device__ __forceinline__ void block_scan(int32_t x, int32_t &before, int32_t &total, int32_t *wsum) {

@@ -2,8 +2,8 @@
 // the dispatch order of its tokens (gfx950).
 //
 //  * route_kernel   a group of G lanes holds a token's logits, V a lane, and takes
-//                   the k largest by k reductions of (value, index) over the
-//                   lanes.  A workgroup has B <= 64 tokens; a token picks an
+//                   the k largest by k reductions over the lanes, of the value and
+//                   then of the index of those that have it.  A workgroup has B <= 64 tokens; a token picks an
 //                   expert once at most, so one 64-bit word an expert in LDS,
 //                   with a bit a token, is its histogram and, below a token's
 //                   bit, that token's place among the workgroup's.
@@ -28,76 +28,90 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 32;
-constexpr int kTokens = 16;      // of a workgroup at a time
 constexpr int kPlaceThreads = 1024;
 constexpr int kSumBlocks = 256;  // workgroups whose counts every workgroup sums by itself
 
-template <int N>
-__device__ __forceinline__ int ror(int v) {
-    return __builtin_amdgcn_update_dpp(0, v, 0x120 + N, 0xF, 0xF, false);
+// v of the lane that CTRL names (DPP).  ROWS: the rows of 16 lanes that take it, the
+// others keep v.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp(int v) {
+    if constexpr (ROWS == 0xF) return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, ROWS, 0xF, false);
 }
-template <int N>
-__device__ __forceinline__ float ror(float v) {
-    return __int_as_float(ror<N>(__float_as_int(v)));
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(dpp<CTRL, ROWS>(__float_as_int(v)));
 }
-template <int N>
-__device__ __forceinline__ double ror(double v) {
-    return __hiloint2double(ror<N>(__double2hiint(v)), ror<N>(__double2loint(v)));
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp(double v) {
+    return __hiloint2double(dpp<CTRL, ROWS>(__double2hiint(v)), dpp<CTRL, ROWS>(__double2loint(v)));
+}
+__device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ float lane_of(float v, int lane) { return __int_as_float(lane_of(__float_as_int(v), lane)); }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    return __hiloint2double(lane_of(__double2hiint(v), lane), lane_of(__double2loint(v), lane));
 }
 
-// op over the G lanes of an aligned group, in every lane of it; op is
-// idempotent, so four rotations of a row of 16 lanes cover it.
+// v of the last lane of the G (16, 32, 64) that this one belongs to, for all of them.
+template <int G, class T>
+__device__ __forceinline__ T from_last(T v) {
+    if constexpr (G == 64) return lane_of(v, 63);
+    if constexpr (G == 32) {
+        const T a = lane_of(v, 31), b = lane_of(v, 63);
+        return pick((threadIdx.x & 32) != 0, b, a);
+    }
+    return v;   // (every lane of a row of 16 has it)
+}
+
+constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;   // rotations of a row of 16 lanes
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143;   // a row's last lane to the next, lane 31 to the upper half
+
+// op over the G lanes of an aligned group, in every lane of it; op is idempotent,
+// so four rotations of a row of 16 lanes cover it.
 template <int G, class T, class Op>
 __device__ __forceinline__ T reduce(T v, Op op) {
-    v = op(v, ror<1>(v));
-    v = op(v, ror<2>(v));
-    v = op(v, ror<4>(v));
-    v = op(v, ror<8>(v));
-    if constexpr (G >= 32) v = op(v, __shfl_xor(v, 16));
-    if constexpr (G >= 64) v = op(v, __shfl_xor(v, 32));
-    return v;
+    v = op(v, dpp<kRor1>(v));
+    v = op(v, dpp<kRor2>(v));
+    v = op(v, dpp<kRor4>(v));
+    v = op(v, dpp<kRor8>(v));
+    if constexpr (G >= 32) v = op(v, dpp<kBcast15, 0xA>(v));
+    if constexpr (G >= 64) v = op(v, dpp<kBcast31, 0xC>(v));
+    return from_last<G>(v);
 }
 
+// The sum over the G lanes, in every lane of them: the same order for all.
 template <int G>
 __device__ __forceinline__ double sum(double v) {
-#pragma unroll
-    for (int d = 1; d < G; d <<= 1) v += __shfl_xor(v, d);
+    v += dpp<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+    v += dpp<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+    v += dpp<0x141>(v);   // row_half_mirror
+    v += dpp<0x140>(v);   // row_mirror
+    if constexpr (G == 32) {
+        const double a = lane_of(v, 0) + lane_of(v, 16), b = lane_of(v, 32) + lane_of(v, 48);
+        return pick((threadIdx.x & 32) != 0, b, a);
+    }
+    if constexpr (G == 64) return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
     return v;
-}
-
-// Takes (ov, oi) if it is larger, or equal with a lower index.
-template <class T>
-__device__ __forceinline__ void take(T &v, int &i, T ov, int oi) {
-    const bool better = ov > v || (ov == v && oi < i);
-    v = better ? ov : v;
-    i = better ? oi : i;
 }
 
 template <class T>
 __device__ __forceinline__ T larger(T a, T b) {
-    return a > b ? a : b;
+    return pick(a > b, a, b);
+}
+template <>
+__device__ __forceinline__ double larger(double a, double b) {
+    return fmax(a, b);
 }
 template <class T>
 __device__ __forceinline__ T smaller(T a, T b) {
-    return a < b ? a : b;
-}
-
-// The largest value and its index over the G lanes, in every lane of them.
-template <int G, class T>
-__device__ __forceinline__ void best_of(T &v, int &i) {
-    take(v, i, ror<1>(v), ror<1>(i));
-    take(v, i, ror<2>(v), ror<2>(i));
-    take(v, i, ror<4>(v), ror<4>(i));
-    take(v, i, ror<8>(v), ror<8>(i));
-    if constexpr (G >= 32) take(v, i, __shfl_xor(v, 16), __shfl_xor(i, 16));
-    if constexpr (G >= 64) take(v, i, __shfl_xor(v, 32), __shfl_xor(i, 32));
+    return pick(a < b, a, b);
 }
 
 // A logit's place in the order, as a signed word: -infinity and NaN the lowest,
 // +infinity as the largest finite value, both zeros alike; kTaken is below all.
 constexpr int32_t kTaken = INT_MIN;
 __device__ __forceinline__ int32_t order_of(float l) {
-    const float f = (l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY) + 0.0f;
+    const float f = pick(l > -INFINITY, fminf(l, FLT_MAX), -INFINITY) + 0.0f;
     const int32_t s = __float_as_int(f);
     return s ^ ((s >> 31) & 0x7FFFFFFF);
 }
@@ -105,28 +119,44 @@ __device__ __forceinline__ float logit_of(int32_t order) {
     return __int_as_float(order ^ ((order >> 31) & 0x7FFFFFFF));
 }
 
-// exp(l - m), or 1 / (1 + exp(-l)); 0 for NaN and -infinity.
+// exp(l - m); 0 for NaN and -infinity.
+__device__ __forceinline__ double softmax_score(float l, float m) {
+    const double e = exp((double)fminf(l, FLT_MAX) - (double)m);
+    return pick(l > -INFINITY, e, 0.0);
+}
+
+// 1 / (1 + exp(-l)), as t / (1 + t) with t = exp(l) where l is negative: t is at most
+// 1, so nothing overflows and the quotient needs no more than the hardware's
+// reciprocal of a value in [1, 2], corrected twice.  0 for NaN and -infinity.
+__device__ __forceinline__ double sigmoid_score(float l) {
+    const double t = exp(-(double)fminf(fabsf(l), FLT_MAX)), d = 1.0 + t;
+    double r = __builtin_amdgcn_rcp(d);
+    r = fma(fma(-d, r, 1.0), r, r);
+    r = fma(fma(-d, r, 1.0), r, r);
+    return pick(l > -INFINITY, pick(l >= 0.0f, r, t * r), 0.0);
+}
 __device__ __forceinline__ double score_of(float l, float m, bool sigmoid) {
-    if (!(l > -INFINITY)) return 0.0;
-    const double x = (double)fminf(l, FLT_MAX);
-    return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)m);
+    return sigmoid ? sigmoid_score(l) : softmax_score(l, m);
 }
 
-__device__ __forceinline__ float load_logit(const RouteArgs &p, const void *row, int e) {
-    return p.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(row)[e]) : static_cast<const float *>(row)[e];
+// Four logits from a place that is aligned to them.
+__device__ __forceinline__ void load_logits4(const RouteArgs &p, const void *row, int e, float *l) {
+    if (p.bf16) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + e);
+        l[0] = bf16_bits_to_f32(v.x & 0xFFFFu), l[1] = bf16_bits_to_f32(v.x >> 16);
+        l[2] = bf16_bits_to_f32(v.y & 0xFFFFu), l[3] = bf16_bits_to_f32(v.y >> 16);
+    } else {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(row) + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[i] = v[i];
+    }
 }
-
 // Exclusive prefix of counts[0 .. E) over the workgroup into starts, and the
 // total: E <= the number of threads.  All threads call it.
 __device__ __forceinline__ void scan_experts(int32_t count, int32_t E, int32_t *starts, int32_t *wave_sums,
                                              int32_t *offsets) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int32_t x = count;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int32_t y = __shfl_up(x, d);
-        x += lane >= d ? y : 0;
-    }
+    const int32_t x = wave_incl_scan(count);
     if (lane == 63) wave_sums[wave] = x;
     __syncthreads();
     int32_t before = 0;
@@ -144,7 +174,7 @@ __device__ __forceinline__ void scan_experts(int32_t count, int32_t E, int32_t *
 // One token on G lanes.  lane's experts: e0 + [0, count).
 template <int G, int V, bool BIAS>
 __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t_local, int lane, uint64_t *mask,
-                                            uint16_t *picks) {
+                                            uint16_t *picks, float *pick_logits) {
     using Val = typename std::conditional<BIAS, double, int32_t>::type;
     constexpr int kNone = INT_MAX;
     const Val taken = BIAS ? (Val)-INFINITY : (Val)kTaken;   // below every choice
@@ -156,9 +186,25 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t
     const int count = g < p.groups ? min(each, n - sub * each) : 0;
     const void *row = p.bf16 ? static_cast<const void *>(static_cast<const uint16_t *>(p.logits) + t * p.ldl)
                              : static_cast<const void *>(static_cast<const float *>(p.logits) + t * p.ldl);
-    float l[V];
+    // all loads at once, those of experts that are not there from one that is
+    float l[V], bias[BIAS ? V : 1];
+    auto at = [=](int v) { return min(e0 + max(min(v, count - 1), 0), p.E - 1); };
+    if (V >= 4 && p.fours) {   // count is 0 or a multiple of 4
 #pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = v < count ? load_logit(p, row, e0 + v) : -INFINITY;
+        for (int v = 0; v < V; v += 4) load_logits4(p, row, at(v & ~3) & ~3, l + v);
+    } else if (p.bf16) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = bf16_bits_to_f32(static_cast<const uint16_t *>(row)[at(v)]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = static_cast<const float *>(row)[at(v)];
+    }
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) bias[v] = p.bias[at(v)];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = v < count ? l[v] : -INFINITY;
 
     // the largest logit that counts, and the sum of the exponentials where it is used
     const bool sigmoid = p.score != 0;
@@ -174,36 +220,40 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t
     // the choices; those taken and those of groups that are not kept: `taken`
     Val c[V];
     if constexpr (BIAS) {
-        double part = 0.0;
+        if (sigmoid) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            c[v] = v < count ? score_of(l[v], m, sigmoid) : 0.0;
-            part += c[v];
-        }
-        if (!sigmoid) {
-            total = sum<G>(part);
-            if (!(total > 0.0)) total = 1.0;
-        }
+            for (int v = 0; v < V; ++v) c[v] = sigmoid_score(l[v]);
+        } else {
+            double part = 0.0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (v < count) {
-                const double b = (double)p.bias[e0 + v];
-                const double w = (sigmoid ? c[v] : c[v] / total) + b;
-                c[v] = w > -DBL_MAX ? fmin(w, DBL_MAX) : -DBL_MAX;   // (NaN: the lowest)
-            } else {
-                c[v] = taken;
+            for (int v = 0; v < V; ++v) {
+                c[v] = softmax_score(l[v], m);
+                part += c[v];
             }
+            total = sum<G>(part);
+            total = pick(total > 0.0, total, 1.0);
+            const double inverse = 1.0 / total;
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] *= inverse;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const double w = c[v] + (double)bias[v];
+            c[v] = pick(v < count, pick(w > -DBL_MAX, fmin(w, DBL_MAX), -DBL_MAX), taken);   // (NaN: the lowest)
         }
     } else {
         if (!sigmoid && !p.renormalize) {
             double part = 0.0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) part += v < count && l[v] > -INFINITY ? (double)expf(fminf(l[v], FLT_MAX) - m) : 0.0;
+            for (int v = 0; v < V; ++v) {
+                const float e = expf(fminf(l[v], FLT_MAX) - m);
+                part += (double)pick(l[v] > -INFINITY, e, 0.0f);
+            }
             total = sum<G>(part);
-            if (!(total > 0.0)) total = 1.0;
+            total = pick(total > 0.0, total, 1.0);
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) c[v] = v < count ? order_of(l[v]) : taken;
+        for (int v = 0; v < V; ++v) c[v] = pick(v < count, order_of(l[v]), taken);
     }
 
     if (p.topk_groups < p.groups) {
@@ -229,8 +279,9 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t
         }
         int rank = 0;
         const int base = (threadIdx.x & 63) & ~(G - 1);
+#pragma unroll 4
         for (int o = 0; o < p.groups; ++o) {
-            const double other = __shfl(value, base + o * lanes);
+            const double other = G == 64 ? lane_of(value, o * lanes) : __shfl(value, base + o * lanes);
             rank += other > value || (other == value && o < g) ? 1 : 0;
         }
         if (rank >= p.topk_groups) {
@@ -239,32 +290,43 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t
         }
     }
 
-    int id[2] = {0, 0};   // lane j % G keeps pick j
-    int last = kNone;
+    // k times the largest choice, then the lowest expert that has it; its lane leaves
+    // both the expert and its logit in LDS
+    picks += t_local * p.k;
+    pick_logits += t_local * p.k;
     for (int j = 0; j < p.k; ++j) {
-        Val bv = taken;
-        int bi = kNone;
+        Val most = c[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) most = larger(most, c[v]);
+        most = reduce<G>(most, [](Val a, Val b) { return larger(a, b); });
+        int mine = kNone;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v) mine = pick(c[v] == most, e0 + v, mine);
+        const int expert = reduce<G>(mine, [](int a, int b) { return min(a, b); });
+        float logit = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            c[v] = e0 + v == last ? taken : c[v];
-            const bool better = c[v] > bv;
-            bv = better ? c[v] : bv;
-            bi = better ? e0 + v : bi;
+            c[v] = pick(e0 + v == expert, taken, c[v]);
+            if constexpr (BIAS) logit = pick(e0 + v == expert, l[v], logit);
         }
-        best_of<G>(bv, bi);
-        last = bi;
-        if (lane == (j & (G - 1))) {
-            if (j < G)
-                id[0] = bi;
-            else
-                id[1] = bi;
+        if (mine == expert) {
+            if constexpr (!BIAS) logit = logit_of(most);
+            picks[j] = (uint16_t)expert;
+            pick_logits[j] = logit;
         }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read by other lanes of the wave
+    __builtin_amdgcn_wave_barrier();
+    int id[2] = {0, 0};
     double w[2], all = 0.0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        const int j = lane + i * G;
         w[i] = 0.0;
-        if (lane + i * G < p.k) w[i] = score_of(load_logit(p, row, id[i]), m, sigmoid);
+        if (j < p.k) {
+            id[i] = picks[j];
+            w[i] = score_of(pick_logits[j], m, sigmoid);
+        }
         all += w[i];
     }
     double factor = p.scale / total;
@@ -279,32 +341,33 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t
             p.ids[t * p.k + j] = id[i];
             p.weights[t * p.k + j] = (float)(w[i] * factor);
             atomicOr(reinterpret_cast<unsigned long long *>(mask + id[i]), 1ull << t_local);
-            picks[t_local * p.k + j] = (uint16_t)id[i];
         }
     }
 }
 
 __device__ __forceinline__ int below(uint64_t mask, int t) { return __popcll(mask & ((1ull << t) - 1)); }
 
-// ceil(T / B) workgroups of kTokens groups; SINGLE: one, which places its rows
-// too (T = 0 included).
-template <int G, int V, bool BIAS, bool SINGLE>
-__global__ __launch_bounds__(kTokens *G) void route_kernel(RouteArgs p) {
-    __shared__ uint64_t mask[G * kTokens];   // E <= G V <= the number of threads
+// A workgroup of THREADS / G tokens at a time; ceil(T / B) of them, or SINGLE one,
+// which places its rows too (T = 0 included).
+template <int G, int V, bool BIAS, int THREADS, bool SINGLE>
+__global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs p) {
+    constexpr int kThreads = THREADS;
+    __shared__ uint64_t mask[kThreads];   // E <= G V <= kThreads
     __shared__ uint16_t picks[64 * kMaxTop];
-    __shared__ int32_t starts[SINGLE ? G * kTokens : 1];
+    __shared__ float pick_logits[64 * kMaxTop];
+    __shared__ int32_t starts[SINGLE ? kThreads : 1];
     __shared__ int32_t wave_sums[16];
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * p.block_tokens;
     mask[tid] = 0;
     __syncthreads();
-    for (int i = tid / G; i < p.block_tokens; i += kTokens)
-        if (t0 + i < p.T) route_token<G, V, BIAS>(p, t0 + i, i, tid & (G - 1), mask, picks);
+    for (int i = tid / G; i < p.block_tokens; i += kThreads / G)
+        if (t0 + i < p.T) route_token<G, V, BIAS>(p, t0 + i, i, tid & (G - 1), mask, picks, pick_logits);
     __syncthreads();
     const int32_t count = tid < p.E ? __popcll(mask[tid]) : 0;
     if constexpr (SINGLE) {
         scan_experts(count, p.E, starts, wave_sums, p.offsets);
-        for (int i = tid; i < (int)p.T * p.k; i += kTokens * G) {
+        for (int i = tid; i < (int)p.T * p.k; i += kThreads) {
             const int t = i / p.k, e = picks[i];
             const int32_t r = starts[e] + below(mask[e], t);
             p.row_of[i] = r;
@@ -379,13 +442,21 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs p, int b
         const uint32_t *counts = reinterpret_cast<const uint32_t *>(p.counts);
         uint32_t even = 0, odd = 0, even_before = 0, odd_before = 0;
         if (slice < slices && slice < blocks) {
-            for (int b = slice; b < blocks; b += slices) {
-                const uint32_t w = counts[b * words + col];
-                even += w & 0x00FF00FFu;
-                odd += (w >> 8) & 0x00FF00FFu;
-                if (b < (int)blockIdx.x) {
-                    even_before += w & 0x00FF00FFu;
-                    odd_before += (w >> 8) & 0x00FF00FFu;
+            constexpr int kBatch = 8;   // in flight; past the last: the last, not counted
+            for (int b0 = slice; b0 < blocks; b0 += kBatch * slices) {
+                uint32_t w[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) w[i] = counts[min(b0 + i * slices, blocks - 1) * words + col];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int b = b0 + i * slices;
+                    if (b >= blocks) w[i] = 0;
+                    even += w[i] & 0x00FF00FFu;
+                    odd += (w[i] >> 8) & 0x00FF00FFu;
+                    if (b < (int)blockIdx.x) {
+                        even_before += w[i] & 0x00FF00FFu;
+                        odd_before += (w[i] >> 8) & 0x00FF00FFu;
+                    }
                 }
             }
             const int e = 4 * col;
@@ -409,49 +480,60 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs p, int b
     }
 }
 
-// Lanes a token and values a lane.
-struct RouteShape {
+int block_tokens(int64_t T) { return T <= kSumBlocks * 16 ? 16 : T <= kSumBlocks * 32 ? 32 : 64; }
+
+// Lanes a token, values a lane, and whether one workgroup does it all.
+struct RoutePlan {
     int G, V;
+    bool single;
 };
 
-RouteShape route_shape(int64_t T, int32_t E, int32_t groups, int log_groups) {
+RoutePlan route_plan(int64_t T, int32_t E, int32_t groups, int log_groups) {
     const int n = E / groups;
     auto values = [&](int G) { return G >> log_groups ? (n + (G >> log_groups) - 1) / (G >> log_groups) : 1 << 20; };
-    for (int G : {16, 32, 64}) {
-        if (T <= 1024 && G < 64) continue;
+    auto plan = [&](int G, bool single) {
         const int v = values(G);
-        if (G == 64 && v > 16) return {64, 32};   // 1024 experts in a number of groups that is no power of two
-        if (v <= 16) return {G, v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : v <= 8 ? 8 : 16};
-    }
-    return {0, 0};
+        return RoutePlan{G, v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : v <= 8 ? 8 : v <= 16 ? 16 : 32, single};
+    };
+    // One workgroup of 1024 threads while all its tokens go at once and the values
+    // stay in 128 registers (64 tokens, 128 experts: 7.6 us with 16 lanes a token,
+    // 11.2 with 32 and 17.0 with 64, tokens in turn; 10.9 as two launches).
+    if (T <= 16) return plan(64, true);
+    if (T <= 32 && values(32) <= 8) return plan(32, true);
+    if (T <= 64 && values(16) <= 8) return plan(16, true);
+    // Else few tokens take many lanes, for the time of one; many take few, for fewer
+    // instructions (4096 tokens, 256 experts: 11.3 us with 16, 11.7 32, 12.7 64).
+    for (int G : {16, 32, 64})
+        if ((T > 1024 || G == 64) && (values(G) <= 16 || G == 64)) return plan(G, false);
+    return plan(64, false);
 }
 
 template <int G, int V, bool BIAS>
-hipError_t launch_route(const RouteArgs &p, int64_t blocks, hipStream_t stream) {
-    if (blocks <= 1)
-        hipLaunchKernelGGL((route_kernel<G, V, BIAS, true>), dim3(1), dim3(kTokens * G), 0, stream, p);
+hipError_t launch_route(const RouteArgs &p, bool single, int64_t blocks, hipStream_t stream) {
+    // 32 tokens at once where a workgroup has as many, for two waves a SIMD (16381
+    // tokens, 160 experts: 15.4 us against 21.0)
+    constexpr int kWide = G == 16 ? 512 : 16 * G;
+    if (single)
+        hipLaunchKernelGGL((route_kernel<G, V, BIAS, 1024, true>), dim3(1), dim3(1024), 0, stream, p);
+    else if (p.block_tokens == 16)
+        hipLaunchKernelGGL((route_kernel<G, V, BIAS, 16 * G, false>), dim3((unsigned)blocks), dim3(16 * G), 0, stream, p);
     else
-        hipLaunchKernelGGL((route_kernel<G, V, BIAS, false>), dim3((unsigned)blocks), dim3(kTokens * G), 0, stream, p);
+        hipLaunchKernelGGL((route_kernel<G, V, BIAS, kWide, false>), dim3((unsigned)blocks), dim3(kWide), 0, stream, p);
     return hipGetLastError();
 }
 
 template <int G, bool BIAS>
-hipError_t by_values(int V, const RouteArgs &p, int64_t blocks, hipStream_t stream) {
-    switch (V) {
-        case 1: return launch_route<G, 1, BIAS>(p, blocks, stream);
-        case 2: return launch_route<G, 2, BIAS>(p, blocks, stream);
-        case 4: return launch_route<G, 4, BIAS>(p, blocks, stream);
-        case 8: return launch_route<G, 8, BIAS>(p, blocks, stream);
-        case 16: return launch_route<G, 16, BIAS>(p, blocks, stream);
-        default:
-            if constexpr (G == 64) return launch_route<64, 32, BIAS>(p, blocks, stream);
+hipError_t by_values(const RoutePlan &plan, const RouteArgs &p, int64_t blocks, hipStream_t stream) {
+    switch (plan.V) {
+        case 1: return launch_route<G, 1, BIAS>(p, plan.single, blocks, stream);
+        case 2: return launch_route<G, 2, BIAS>(p, plan.single, blocks, stream);
+        case 4: return launch_route<G, 4, BIAS>(p, plan.single, blocks, stream);
+        case 8: return launch_route<G, 8, BIAS>(p, plan.single, blocks, stream);
+        case 16: return launch_route<G, 16, BIAS>(p, plan.single, blocks, stream);
+        default:   // up to 1024 experts in a number of groups that is no power of two
+            if constexpr (G == 64) return launch_route<64, 32, BIAS>(p, plan.single, blocks, stream);
             return hipErrorInvalidValue;
     }
-}
-
-int block_tokens(int64_t T) {
-    if (T <= 16) return 16;
-    return T <= kSumBlocks * 16 ? 16 : T <= kSumBlocks * 32 ? 32 : 64;
 }
 
 int64_t pad16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -466,13 +548,16 @@ int64_t route_grouped_workspace_bytes(int64_t T, int32_t E) {
 }
 
 hipError_t launch_moe_route_grouped(RouteArgs p, void *workspace, hipStream_t stream) {
-    p.block_tokens = block_tokens(p.T);
     p.log_groups = 0;
     while ((1 << p.log_groups) < p.groups) ++p.log_groups;
     p.pitch = (p.E + 3) / 4 * 4;
+    const RoutePlan plan = route_plan(p.T, p.E, p.groups, p.log_groups);
+    p.block_tokens = plan.single ? 64 : block_tokens(p.T);
     const int64_t blocks = (p.T + p.block_tokens - 1) / p.block_tokens;
-    const RouteShape s = route_shape(p.T, p.E, p.groups, p.log_groups);
-    if (s.G == 0 || !launch_fits(blocks, kPlaceThreads)) return hipErrorInvalidValue;
+    if (!launch_fits(blocks, kPlaceThreads)) return hipErrorInvalidValue;
+    const int n = p.E / p.groups, lanes = plan.G >> p.log_groups, each = (n + lanes - 1) / lanes;
+    p.fours = each % 4 == 0 && n % each == 0 && p.ldl % 4 == 0 &&
+              (reinterpret_cast<uintptr_t>(p.logits) & (p.bf16 ? 7u : 15u)) == 0;
     p.counts = static_cast<uint8_t *>(workspace);
     if (blocks > kSumBlocks) {
         p.totals = reinterpret_cast<int32_t *>(p.counts + pad16(blocks * p.pitch));
@@ -480,14 +565,14 @@ hipError_t launch_moe_route_grouped(RouteArgs p, void *workspace, hipStream_t st
     }
     hipError_t e;
     if (p.bias)
-        e = s.G == 16   ? by_values<16, true>(s.V, p, blocks, stream)
-            : s.G == 32 ? by_values<32, true>(s.V, p, blocks, stream)
-                        : by_values<64, true>(s.V, p, blocks, stream);
+        e = plan.G == 16   ? by_values<16, true>(plan, p, blocks, stream)
+            : plan.G == 32 ? by_values<32, true>(plan, p, blocks, stream)
+                           : by_values<64, true>(plan, p, blocks, stream);
     else
-        e = s.G == 16   ? by_values<16, false>(s.V, p, blocks, stream)
-            : s.G == 32 ? by_values<32, false>(s.V, p, blocks, stream)
-                        : by_values<64, false>(s.V, p, blocks, stream);
-    if (e != hipSuccess || blocks <= 1) return e;
+        e = plan.G == 16   ? by_values<16, false>(plan, p, blocks, stream)
+            : plan.G == 32 ? by_values<32, false>(plan, p, blocks, stream)
+                           : by_values<64, false>(plan, p, blocks, stream);
+    if (e != hipSuccess || plan.single) return e;
     if (p.before) {
         hipLaunchKernelGGL(column_kernel, dim3((unsigned)(p.pitch / 4)), dim3(256), 0, stream, p, blocks);
         e = hipGetLastError();
