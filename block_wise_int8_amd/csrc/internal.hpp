@@ -147,7 +147,8 @@ struct LoraArgs {
     // workgroups that share the candidates (adapters, or rows) of a block of rows;
     // columns of y a workgroup, of K a wave; first column and block of columns of
     // each part, and behind the last
-    int32_t splits, rank_waves, slots, candidates, by_adapter, columns;
+    // (narrow: rows 16 at a time)
+    int32_t splits, rank_waves, slots, candidates, by_adapter, columns, narrow;
     int64_t slice;
     int64_t part_first[kMaxParts + 1];
     int32_t part_blocks[kMaxParts + 1];
