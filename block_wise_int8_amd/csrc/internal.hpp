@@ -143,12 +143,11 @@ struct LoraArgs {
     float *t;                    // [splits, M, ranks]
     int64_t ldx, ldy, M, N, K;
     int32_t L, R, ranks;
-    // the launch's own: workgroups that share K, waves of one that share the ranks;
-    // workgroups that share the candidates (adapters, or rows) of a block of rows;
-    // columns of y a workgroup, of K a wave; first column and block of columns of
-    // each part, and behind the last
-    // (narrow: rows 16 at a time)
-    int32_t splits, rank_waves, slots, candidates, by_adapter, columns, narrow;
+    // the launch's own: blocks of rows; workgroups that share K, waves of one that
+    // share the ranks; workgroups that share the adapters of a block of rows, in
+    // either kernel, and how they do; rows 16 at a time; columns of y a workgroup, of K
+    // a wave; first column and block of columns of each part, and behind the last
+    int32_t blocks, splits, rank_waves, shrink_slots, slots, walk, candidates, by_adapter, narrow, columns;
     int64_t slice;
     int64_t part_first[kMaxParts + 1];
     int32_t part_blocks[kMaxParts + 1];

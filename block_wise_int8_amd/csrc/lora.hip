@@ -9,10 +9,9 @@
 //
 // Rows and adapters.  Both take 64 rows at a time, one a lane; the rows of an
 // adapter are a ballot of the lanes that hold it, pushed together to tiles of 16.
-// Few adapters (64 at most): workgroup `slot` does adapters slot, slot + slots, ...
-// of its rows; more: those whose first row is slot, slot + slots, ...  No row is
-// sorted and nothing is kept between calls; rows of one adapter that lie next to
-// each other make full tiles.
+// One or more workgroups, the slots, share the adapters of such a block.  No row is
+// sorted and nothing is kept between calls; rows of one adapter that lie next to each
+// other make full tiles.
 //
 // Matrix core: 16x16x32 bf16 with t's side transposed in both (ranks, then
 // columns of y, are rows of the result), so that a lane ends up with neighbouring
@@ -54,16 +53,40 @@ __device__ __forceinline__ int adapter_of(const LoraArgs &p, int64_t m0, int lan
     return e >= 0 && e < p.L ? e : -1;
 }
 
-// Candidate i of a block (see the head): whether it is there; then its adapter and
-// the lanes that hold it, as a list: entry l for l < count.  Uniform over the wave.
+// The adapters of a block, each with the lanes that hold it as a list: entry l for
+// l < count.  Uniform over the wave.  Of a few blocks each slot looks at candidates of
+// its own: adapters slot, slot + slots, ..., or, where there are more than 64, rows,
+// which stand for their adapter if no row before does.  Of many it walks over all in
+// the order of their first rows and takes number slot, slot + slots, ..., so that the
+// first slot always has work and the second has where an adapter ends (4096 rows of 6
+// runs: 128 us against 131, of 200 runs, 4096 columns, 96 against 134; but 16 rows of
+// 16 adapters 10.4 against 8.2).
 struct Rows {
     int adapter, count, list;   // list: this lane's entry
 };
-__device__ __forceinline__ bool rows_of(const LoraArgs &p, int mine, int i, int lane, Rows &r) {
-    r.adapter = p.by_adapter ? i : __builtin_amdgcn_readlane(mine, i);
-    if (r.adapter < 0) return false;
-    const uint64_t members = __ballot(mine == r.adapter);
-    if (members == 0 || (!p.by_adapter && __ffsll((unsigned long long)members) - 1 != i)) return false;
+struct Adapters {
+    uint64_t left;   // walk: lanes whose adapter has not come yet
+    int next;        // candidate; walk: number of the next one, modulo slots
+};
+__device__ __forceinline__ bool next_rows(const LoraArgs &p, int slots, int slot, int mine, int lane, Adapters &s, Rows &r) {
+    uint64_t members;
+    for (bool taken = false; !taken;) {
+        if (p.walk) {
+            if (s.left == 0) return false;
+            r.adapter = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)s.left) - 1);
+            members = __ballot(mine == r.adapter);
+            s.left &= ~members;
+            taken = s.next == slot;
+            s.next = s.next + 1 == slots ? 0 : s.next + 1;
+        } else {
+            if (s.next >= p.candidates) return false;
+            r.adapter = p.by_adapter ? s.next : __builtin_amdgcn_readlane(mine, s.next);
+            members = __ballot(mine == r.adapter);
+            taken = r.adapter >= 0 && members != 0 &&
+                    (p.by_adapter || __ffsll((unsigned long long)members) - 1 == s.next);
+            s.next += slots;
+        }
+    }
     r.count = __popcll(members);
     const uint64_t lower = (1ull << lane) - 1;
     const bool in = (members >> lane) & 1;
@@ -80,8 +103,8 @@ __device__ __forceinline__ Rows part_of(const Rows &r, int row0, int lane) {
 // Lanes.  The matrix core wants row l % 16, chunk l / 16 of a tile of 16 rows of 4
 // chunks on lane l, the memory pipe four neighbouring lanes on the four chunks of a
 // row (each lane that goes to another row than the one before costs it a cycle: 138 us
-// against 128 for the second kernel of 4096 rows, 28672 columns, rank 64).  So memory sees lane l at row l / 4,
-// chunk l % 4, and registers change lanes in between.
+// against 128 for the second kernel of 4096 rows, 28672 columns, rank 64).  So memory
+// sees lane l at row l / 4, chunk l % 4, and registers change lanes in between.
 __device__ __forceinline__ int to_core(int lane) { return (4 * (lane & 15) + (lane >> 4)) << 2; }
 __device__ __forceinline__ int to_memory(int lane) { return (16 * (lane & 3) + (lane >> 2)) << 2; }
 
@@ -197,7 +220,7 @@ __device__ __forceinline__ void shrink_rows(const LoraArgs &p, const Rows &r, in
     }
 }
 
-// Workgroup: split of K, fastest; then slot; then block of rows.  NARROW: rows are
+// Workgroup: split of K, fastest; then block of rows; then slot.  NARROW: rows are
 // taken 16 at a time, in fewer registers, for more waves.
 template <int NR, bool NARROW, bool ODD>
 __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs p) {
@@ -205,11 +228,11 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
     const int lane = threadIdx.x & 63;
     const uint32_t id = blockIdx.x, rest = id / (uint32_t)p.splits;
     const int split = (int)(id - rest * p.splits);
-    const int64_t m0 = (int64_t)(rest / (uint32_t)p.slots) * kRows;
+    const int slot = (int)(rest / (uint32_t)p.blocks);
+    const int64_t m0 = (int64_t)(rest - slot * (uint32_t)p.blocks) * kRows;
     const int mine = adapter_of(p, m0, lane);
-    for (int i = (int)(rest % (uint32_t)p.slots); i < p.candidates; i += p.slots) {
-        Rows r;
-        if (!rows_of(p, mine, i, lane, r)) continue;
+    Adapters s = {__ballot(mine >= 0), p.walk ? 0 : slot};
+    for (Rows r; next_rows(p, p.shrink_slots, slot, mine, lane, s, r);) {
         if constexpr (NARROW) {
             for (int row0 = 0; row0 < r.count; row0 += 16)
                 shrink_rows<1, NR, ODD>(p, part_of(r, row0, lane), m0, split, meet);
@@ -364,7 +387,7 @@ __device__ __forceinline__ void expand_rows(const LoraArgs &p, const Rows &r, in
     }
 }
 
-// Workgroup: block of columns, fastest; then slot; then block of rows.  NARROW as
+// Workgroup: block of columns, fastest; then block of rows; then slot.  NARROW as
 // above.
 template <int NM, bool TWICE, bool NARROW, bool ODD>
 __global__ __launch_bounds__(64 * kExpandWaves, NM <= 4 ? (NARROW ? 4 : 3) : 2) void lora_expand_kernel(LoraArgs p) {
@@ -380,11 +403,11 @@ __global__ __launch_bounds__(64 * kExpandWaves, NM <= 4 ? (NARROW ? 4 : 3) : 2) 
         if (cb >= p.part_blocks[i]) part = i;   // (parts that are not there begin past all blocks)
     const int64_t n0 = p.part_first[part] + (int64_t)(cb - p.part_blocks[part]) * p.columns;
     const int64_t end = min(n0 + p.columns, p.part_first[part + 1]);
-    const int64_t m0 = (int64_t)(rest / (uint32_t)p.slots) * kRows;
+    const int slot = (int)(rest / (uint32_t)p.blocks);
+    const int64_t m0 = (int64_t)(rest - slot * (uint32_t)p.blocks) * kRows;
     const int mine = adapter_of(p, m0, lane);
-    for (int i = (int)(rest % (uint32_t)p.slots); i < p.candidates; i += p.slots) {
-        Rows r;
-        if (!rows_of(p, mine, i, lane, r)) continue;
+    Adapters s = {__ballot(mine >= 0), p.walk ? 0 : slot};
+    for (Rows r; next_rows(p, p.slots, slot, mine, lane, s, r);) {
         for (int row0 = 0; row0 < r.count; row0 += kTile) {
             const int count = min(r.count - row0, kTile);
             __syncthreads();   // the last tile is read
@@ -428,7 +451,7 @@ int splits_of(int64_t M, int64_t K, int32_t ranks, int64_t *slice) {
 
 template <int NR, bool ODD>
 hipError_t launch_shrink(const LoraArgs &p, hipStream_t stream) {
-    const int64_t groups = blocks_of(p.M) * p.slots * p.splits;
+    const int64_t groups = (int64_t)p.blocks * p.shrink_slots * p.splits;
     if (!launch_fits(groups, 64 * kShrinkWaves)) return hipErrorInvalidValue;
     if (p.narrow)
         hipLaunchKernelGGL((lora_shrink_kernel<NR, true, ODD>), dim3((unsigned)groups), dim3(64 * kShrinkWaves), 0, stream, p);
@@ -449,7 +472,7 @@ hipError_t shrink(const LoraArgs &p, int tiles, hipStream_t stream) {
 
 template <int NM, bool TWICE, bool ODD>
 hipError_t launch_expand(const LoraArgs &p, hipStream_t stream) {
-    const int64_t groups = blocks_of(p.M) * p.slots * p.part_blocks[kMaxParts];
+    const int64_t groups = (int64_t)p.blocks * p.slots * p.part_blocks[kMaxParts];
     if (!launch_fits(groups, 64 * kExpandWaves)) return hipErrorInvalidValue;
     if (p.narrow)
         hipLaunchKernelGGL((lora_expand_kernel<NM, TWICE, true, ODD>), dim3((unsigned)groups), dim3(64 * kExpandWaves), 0,
@@ -496,11 +519,13 @@ hipError_t launch_lora_add(LoraArgs p, const int64_t *part_columns, int32_t part
     p.narrow = p.M <= 16 || p.M <= 2ll * p.L;
     p.by_adapter = p.L <= kRows;
     p.candidates = p.by_adapter ? p.L : kRows;
-    // Workgroups for the candidates of a block: all at once while the grid is small;
-    // of long batches one or a few, since one without work costs its launch (4096
-    // rows of 6 runs, 8 adapters: 171 us with one, 187 two, 226 eight).
-    p.slots = blocks <= 2 ? kRows : blocks <= 16 ? 16 : p.by_adapter ? 1 : 4;
-    p.slots = p.slots < p.candidates ? p.slots : p.candidates;
+    // Workgroups for the adapters of a block: all at once while the grid is small; of
+    // long batches few, since one without work costs its launch.
+    p.walk = blocks > (p.L <= 16 ? 4 : 16);
+    auto slots = [&](int s) { return s < p.candidates ? s : p.candidates; };
+    p.slots = slots(blocks <= 2 ? kRows : blocks <= 16 ? 16 : p.by_adapter ? 1 : 4);
+    p.shrink_slots = blocks <= 16 ? p.slots : slots(p.by_adapter ? 2 : 4);
+    p.blocks = (int32_t)blocks;
     // Columns of a workgroup: more mean fewer sums over the splits (64 rows of their
     // own adapters, N = 6144: 13.4 us with 128, 8.5 256, 6.4 512, 7.1 1024), fewer
     // keep small grids wide (333 rows, N = 5000: 7.5, 6.6, 7.2, 9.3).
