@@ -3,15 +3,21 @@
 //
 //  * route_kernel   a group of G lanes holds a token's logits, V a lane, and takes
 //                   the k largest by k reductions over the lanes, of the value and
-//                   then of the index of those that have it.  A workgroup has B <= 64 tokens; a token picks an
-//                   expert once at most, so one 64-bit word an expert in LDS,
-//                   with a bit a token, is its histogram and, below a token's
-//                   bit, that token's place among the workgroup's.
+//                   then of the index of those that have it.  A workgroup has
+//                   B <= 64 tokens; a token picks an expert once at most, so one
+//                   64-bit word an expert in LDS, with a bit a token, is its
+//                   histogram and, below a token's bit, that token's place among
+//                   the workgroup's.
 //  * place_kernel   a workgroup for the same B tokens: sums the counts of all
 //                   workgroups (an expert's start) and of those before it, and
 //                   writes the rows.  One workgroup's tokens are placed by
 //                   route_kernel itself.
 //  * column_kernel  past kSumBlocks workgroups: those sums, once for all.
+//
+// Bound by the instructions of the picks, and by the latency of their chain where
+// tokens are few: 1 token of 256 experts in 8 groups, top 8, 6.3 us, 64 of 128 7.7,
+// 4096 of 256 14.7 (11 and 5 of the second kernel), 16381 of 160 19.7.  The logits
+// would take 0.8 and 1.1.
 //
 // Lanes and groups: the experts of a group lie on G / 2^ceil(log2 groups)
 // neighbouring lanes, so that a group's value is a reduction over those.
