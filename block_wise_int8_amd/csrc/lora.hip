@@ -452,10 +452,12 @@ int splits_of(int64_t M, int64_t K, int32_t ranks, int64_t *slice) {
     return (int)splits;
 }
 
+int64_t shrink_groups(const LoraArgs &p) { return (int64_t)p.blocks * p.shrink_slots * p.splits; }
+int64_t expand_groups(const LoraArgs &p) { return (int64_t)p.blocks * p.slots * p.part_blocks[kMaxParts]; }
+
 template <int NR, bool ODD>
 hipError_t launch_shrink(const LoraArgs &p, hipStream_t stream) {
-    const int64_t groups = (int64_t)p.blocks * p.shrink_slots * p.splits;
-    if (!launch_fits(groups, 64 * kShrinkWaves)) return hipErrorInvalidValue;
+    const int64_t groups = shrink_groups(p);
     if (p.narrow)
         hipLaunchKernelGGL((lora_shrink_kernel<NR, true, ODD>), dim3((unsigned)groups), dim3(64 * kShrinkWaves), 0, stream, p);
     else
@@ -475,8 +477,7 @@ hipError_t shrink(const LoraArgs &p, int tiles, hipStream_t stream) {
 
 template <int NM, bool TWICE, bool ODD>
 hipError_t launch_expand(const LoraArgs &p, hipStream_t stream) {
-    const int64_t groups = (int64_t)p.blocks * p.slots * p.part_blocks[kMaxParts];
-    if (!launch_fits(groups, 64 * kExpandWaves)) return hipErrorInvalidValue;
+    const int64_t groups = expand_groups(p);
     if (p.narrow)
         hipLaunchKernelGGL((lora_expand_kernel<NM, TWICE, true, ODD>), dim3((unsigned)groups), dim3(64 * kExpandWaves), 0,
                            stream, p);
@@ -516,7 +517,6 @@ hipError_t launch_lora_add(LoraArgs p, const int64_t *part_columns, int32_t part
     rank_shape(p.ranks, &tiles, &rank_waves);
     p.rank_waves = rank_waves;
     const int64_t blocks = blocks_of(p.M);
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
     // 16 rows at a time where an adapter is likely to have no more (64 rows, 64
     // adapters of 48 ranks: 15.0 us against 16.9; but 17.1 against 11.4 where all 64
     // rows have the only one, 22.2 against 14.7 for 512 rows of 8).
@@ -550,6 +550,8 @@ hipError_t launch_lora_add(LoraArgs p, const int64_t *part_columns, int32_t part
     }
     p.part_first[kMaxParts] = first;
     p.part_blocks[kMaxParts] = block;
+    if (!launch_fits(shrink_groups(p), 64 * kShrinkWaves) || !launch_fits(expand_groups(p), 64 * kExpandWaves))
+        return hipErrorInvalidValue;
     const bool odd_k = p.K % 8 != 0 || p.ldx % 8 != 0 || off(p.x);
     const hipError_t e = odd_k ? shrink<true>(p, tiles, stream) : shrink<false>(p, tiles, stream);
     if (e != hipSuccess) return e;

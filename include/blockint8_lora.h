@@ -45,14 +45,16 @@ extern "C" {
  * Rows are taken 64 at a time, those of one adapter together: a batch whose rows
  * of one adapter lie next to each other reads the adapters least often.  Adapters
  * of smaller rank are padded with zeros (in a or in b, and no NaN or infinity in
- * the other).  x and y may not overlap.
+ * the other).  An infinity in b may give NaN where the formula gives an infinity: it
+ * meets both of t's values, of which one may be 0.  x and y may not overlap.
  *
  * Errors: NULL pointer (M > 0; scales may be) -> BI8_ERR_NULL; M < 0, N, K, L, R
  * or parts < 1, K, N, ldx or ldy > BI8_MAX_K, L > 2^24, parts > BI8_MAX_PARTS,
  * parts * R > BI8_MAX_RANKS, a width < 1 or another sum than N, ldx < K, ldy < N,
  * a workspace too small -> BI8_ERR_SHAPE; R % 8 != 0, a, b or workspace not
  * 16-byte, x or y not 2-byte, scales or adapter not 4-byte aligned ->
- * BI8_ERR_ALIGN.
+ * BI8_ERR_ALIGN; more rows than launches of 2^32 threads hold (by N, L
+ * and parts) -> BI8_ERR_HIP, and nothing is launched.
  */
 int32_t blockint8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b, const float *scales,
                            const int32_t *adapter, uint16_t *y, int64_t ldy, int64_t M, int64_t N, int64_t K, int32_t L,

@@ -137,3 +137,15 @@ def test_workspace_sizes():
     assert size(0, 64, 8) == size(-1, 64, 8) == size(5, 0, 8) == size(5, 64, 12) == size(5, 64, 264) == 0
     assert size(5, 64, 136, 2) == size(5, 64, 8, 0) == size(5, 64, 8, 5) == size(1 << 31, 64, 8) == 0
     assert size(5, 64, 16, 2) == 5 * 32 * 4 and size(1, 4096, 16) % (16 * 4) == 0
+
+
+def test_grids_of_too_many_threads_are_refused():
+    """Before either launch (the runtime would report no error and run the grid modulo 2^32)."""
+    lib, P, HIP = bi8.load(), 0x10000, 5
+    for M, L, parts in ((1 << 29, 1, (1,)),        # the first product's grid
+                        (1 << 28, 1, (1,) * 4),    # the second's: a workgroup at least for each part
+                        (1 << 27, 100, (4,))):
+        n = lib.blockint8_lora_add_workspace_size(M, 1, 8, len(parts))
+        status = lib.blockint8_lora_add(P, 1, P, P, None, P, P, sum(parts), M, sum(parts), 1, L, 8, len(parts),
+                                        (ctypes.c_int64 * len(parts))(*parts), P, n, None)
+        assert (status, b"invalid" in lib.blockint8_last_error().lower()) == (HIP, True), (M, L, parts)
