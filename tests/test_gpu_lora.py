@@ -220,3 +220,17 @@ def test_captured_and_replayed(M):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, bi8.lora_add(ys[r].clone(), xs[r], a, b, ids[r], s))
+
+
+@pytest.mark.parametrize("M,N,K,L,R,parts", [
+    (64, 264, 96, 40, 16, None), (70, 200, 72, 70, 64, (100, 100)), (100, 130, 100, 60, 24, None), (150, 96, 64, 90, 136, None),
+    (130, 72, 136, 80, 256, None), (1100, 72, 40, 600, 8, None), (33, 1030, 1000, 20, 128, None)])
+def test_many_adapters_one_of_them_crowded(M, N, K, L, R, parts):
+    """More adapters than half the rows, and half the rows on one: rows go 16 at a time, and some have to go again."""
+    rng = wl.rng_for((127, M, N, K))
+    x, a, b, y, s = make(rng, M, N, K, L, R, 1 if parts is None else len(parts))
+    adapter = rng.integers(0, L, M).astype(np.int32)
+    adapter[rng.permutation(M)[: M // 2]] = L - 1
+    yd = bf16_to_dev(y)
+    bi8.lora_add(yd, bf16_to_dev(x), bf16_to_dev(a), bf16_to_dev(b), to_dev(adapter), to_dev(s), parts)
+    check(bf16_bits(yd), x, a, b, y, s, adapter, parts or (N,))
