@@ -126,6 +126,16 @@ __device__ __forceinline__ u32x4 load_at(__amdgpu_buffer_rsrc_t r, uint32_t offs
     return __builtin_amdgcn_raw_buffer_load_b128(r, (int)offset, (int)(2 * element), 0);
 }
 
+// Stores have no offset in a scalar register.  A store of four registers goes on reading
+// them behind its issue; the compiler keeps writes of them two wait states away, but not
+// behind a store with a scalar offset, where it takes them to be free at once.  They are
+// not: the next instruction's 2^31 (the offset of a load that is not there) was stored in
+// the place of the first register, two values of y as zeros, in a quarter of all calls of
+// 333 rows and 5000 columns.
+__device__ __forceinline__ void store_at(__amdgpu_buffer_rsrc_t r, uint32_t offset, const u32x4 &v) {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)offset, 0, 0);
+}
+
 // J tiles of 16 rows times the wave's NR tiles of 16 ranks from rank0 on, over the
 // K columns [first, last) of its slice.  kAhead steps of 32 columns are on their way
 // in a ring of registers while the oldest is multiplied.
@@ -375,7 +385,7 @@ __device__ __forceinline__ void expand_rows(const LoraArgs &p, const Rows &r, in
             if constexpr (ODD) {
                 if (yoff[j] != kOobOffset && 8 * g < left) store_bf16x8(y + n + yoff[j] / 2, o, left - 8 * g);
             } else {
-                __builtin_amdgcn_raw_buffer_store_b128(o, ybuf, (int)(8 * g < left ? yoff[j] : kOobOffset), 2 * n, 0);
+                store_at(ybuf, 8 * g < left ? yoff[j] + 2u * n : kOobOffset, o);
             }
         }
     };
