@@ -142,7 +142,7 @@ int32_t blockint8_moe_route_grouped(const void *logits, int32_t logits_bf16, int
     BI8_TRY(check_align(fn, "sorted_token", sorted_token, 4));
     BI8_TRY(check_align(fn, "expert_offsets", expert_offsets, 4));
     BI8_TRY(check_align(fn, "row_of", row_of, 4));
-    const int64_t need = T > 0 ? bi8::route_grouped_workspace_bytes(T, E) : 0;
+    const int64_t need = T > 0 ? bi8::route_grouped_workspace_need(T, E) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn,
                            (long long)(workspace ? workspace_bytes : 0), (long long)need);
@@ -202,7 +202,7 @@ int32_t blockint8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     BI8_TRY(check_align(fn, "scales", scales, 4));
     BI8_TRY(check_align(fn, "adapter", adapter, 4));
     BI8_TRY(check_align(fn, "y", y, 2));
-    const int64_t need = bi8::lora_workspace_bytes(M, K, parts * R);
+    const int64_t need = bi8::lora_workspace_need(M, K, parts * R);
     if (workspace_bytes < need)
         return fail_status(BI8_ERR_SHAPE, "%s: workspace_bytes = %lld < %lld", fn, (long long)workspace_bytes,
                            (long long)need);

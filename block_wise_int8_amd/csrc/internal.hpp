@@ -130,7 +130,8 @@ struct RouteArgs {
     uint8_t *counts;
     int32_t *before, *totals;
 };
-int64_t route_grouped_workspace_bytes(int64_t T, int32_t E);
+int64_t route_grouped_workspace_need(int64_t T, int32_t E);    // of a call
+int64_t route_grouped_workspace_bytes(int64_t T, int32_t E);   // of any call of up to T tokens
 hipError_t launch_moe_route_grouped(RouteArgs p, void *workspace, hipStream_t stream);
 
 // Low-rank adapters beside a projection (lora.hip).
@@ -152,7 +153,8 @@ struct LoraArgs {
     int64_t part_first[kMaxParts + 1];
     int32_t part_blocks[kMaxParts + 1];
 };
-int64_t lora_workspace_bytes(int64_t M, int64_t K, int32_t ranks);
+int64_t lora_workspace_need(int64_t M, int64_t K, int32_t ranks);    // of a call
+int64_t lora_workspace_bytes(int64_t M, int64_t K, int32_t ranks);   // of any call of up to M rows
 hipError_t launch_lora_add(LoraArgs p, const int64_t *part_columns, int32_t parts, hipStream_t stream);
 
 // Norm and rotation of query and key heads (heads.hip).

@@ -23,6 +23,8 @@
 // rows, K = 4096, 28672 columns, rank 64 in 6 runs: 28 to 35 us and about 115 (y alone,
 // read and written in the same order, 88); 64 rows of 64 adapters, 6144 columns, rank
 // 16: 8.5 and 7.2 (40 MB of adapters); 1 row 4.5 and 4.8, the latency of two launches.
+#include <algorithm>
+
 #include "codes.hpp"
 #include "internal.hpp"
 
@@ -35,6 +37,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kRows = 64;   // of a block of rows: one a lane
 constexpr int kShrinkWaves = 8;
 constexpr int kExpandWaves = 4;
+constexpr int kMaxSplits = 8;   // workgroups that share K
 constexpr int kColumns = 32;   // of a wave at a time
 
 __device__ __forceinline__ f32x4 mfma(const u32x4 &a, const u32x4 &b, f32x4 c) {
@@ -455,7 +458,7 @@ int splits_of(int64_t M, int64_t K, int32_t ranks, int64_t *slice) {
     rank_shape(ranks, &tiles, &waves);
     const int64_t slices = kShrinkWaves / waves, most = (K + 64 * slices - 1) / (64 * slices);
     int64_t splits = 256 / blocks_of(M);
-    splits = splits < 1 ? 1 : splits > 8 ? 8 : splits;
+    splits = splits < 1 ? 1 : splits > kMaxSplits ? kMaxSplits : splits;
     if (splits > most) splits = most;
     const int64_t per = (K + splits * slices - 1) / (splits * slices);
     *slice = (per + 31) / 32 * 32;
@@ -516,9 +519,20 @@ hipError_t expand(const LoraArgs &p, hipStream_t stream) {
 
 }  // namespace
 
-int64_t lora_workspace_bytes(int64_t M, int64_t K, int32_t ranks) {
+int64_t lora_workspace_need(int64_t M, int64_t K, int32_t ranks) {
     int64_t slice;
     return splits_of(M, K, ranks, &slice) * M * ranks * 4;
+}
+
+// The most that a batch of up to M rows needs: each number of splits above M's at the
+// last batch that has it.
+int64_t lora_workspace_bytes(int64_t M, int64_t K, int32_t ranks) {
+    int64_t most = lora_workspace_need(M, K, ranks);
+    for (int64_t splits = 2; splits <= kMaxSplits; ++splits) {
+        const int64_t last = 256 / splits * kRows;
+        if (last < M) most = std::max(most, lora_workspace_need(last, K, ranks));
+    }
+    return most;
 }
 
 hipError_t launch_lora_add(LoraArgs p, const int64_t *part_columns, int32_t parts, hipStream_t stream) {

@@ -21,6 +21,7 @@
 //
 // Lanes and groups: the experts of a group lie on G / 2^ceil(log2 groups)
 // neighbouring lanes, so that a group's value is a reduction over those.
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -546,11 +547,18 @@ int64_t pad16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-int64_t route_grouped_workspace_bytes(int64_t T, int32_t E) {
+int64_t route_grouped_workspace_need(int64_t T, int32_t E) {
     const int64_t blocks = (T + block_tokens(T) - 1) / block_tokens(T), pitch = (E + 3) / 4 * 4;
     if (blocks <= 1) return 0;
     const int64_t counts = pad16(blocks * pitch);
     return blocks <= kSumBlocks ? counts : counts + pad16(4 * pitch) + 4 * blocks * pitch;
+}
+
+// The most that a batch of up to T tokens needs: workgroups have twice the tokens past
+// 2^12 and 2^13, and are half as many.
+int64_t route_grouped_workspace_bytes(int64_t T, int32_t E) {
+    const int64_t most = route_grouped_workspace_need(T, E);
+    return T > kSumBlocks * 16 ? std::max(most, route_grouped_workspace_need(kSumBlocks * 16, E)) : most;
 }
 
 hipError_t launch_moe_route_grouped(RouteArgs p, void *workspace, hipStream_t stream) {

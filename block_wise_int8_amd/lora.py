@@ -20,7 +20,7 @@ def declare(lib) -> None:
 
 
 def lora_add_workspace_size(M: int, K: int, R: int, parts: int = 1) -> int:
-    """Bytes of workspace ``lora_add`` needs for M rows of K columns and adapters of rank R in each part."""
+    """Bytes of workspace ``lora_add`` needs for up to M rows of K columns and adapters of rank R in each part."""
     return int(_bi8.load().blockint8_lora_add_workspace_size(M, K, R, parts))
 
 

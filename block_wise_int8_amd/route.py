@@ -21,7 +21,7 @@ def declare(lib) -> None:
 
 
 def moe_route_grouped_workspace_size(T: int, E: int) -> int:
-    """Bytes of workspace ``moe_route_grouped`` needs for T tokens (0: none)."""
+    """Bytes of workspace ``moe_route_grouped`` needs for up to T tokens (0: none)."""
     return int(_bi8.load().blockint8_moe_route_grouped_workspace_size(T, E))
 
 

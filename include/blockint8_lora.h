@@ -61,7 +61,8 @@ int32_t blockint8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
                            int32_t R, int32_t parts, const int64_t *part_columns, void *workspace,
                            int64_t workspace_bytes, void *stream);
 
-/* 0 for sizes that blockint8_lora_add rejects, and for M = 0. */
+/* Enough for any batch of up to M rows: it does not fall as M grows.  0 for sizes that
+ * blockint8_lora_add rejects, and for M = 0. */
 int64_t blockint8_lora_add_workspace_size(int64_t M, int64_t K, int32_t R, int32_t parts);
 
 #ifdef __cplusplus

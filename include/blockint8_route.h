@@ -65,7 +65,8 @@ int32_t blockint8_moe_route_grouped(const void *logits, int32_t logits_bf16, int
                                     float *topk_weights, int32_t *sorted_token, int32_t *expert_offsets,
                                     int32_t *row_of, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* 0 for few tokens and for sizes that blockint8_moe_route_grouped rejects. */
+/* Enough for any batch of up to T tokens: it does not fall as T grows.  0 for few tokens
+ * and for sizes that blockint8_moe_route_grouped rejects. */
 int64_t blockint8_moe_route_grouped_workspace_size(int64_t T, int32_t E);
 
 /*
@@ -89,7 +90,8 @@ int32_t blockint8_moe_layer_fp8_routed(int32_t variant, const uint16_t *x, int64
                                        int32_t k, int32_t block_n, int32_t block_k, void *workspace,
                                        int64_t workspace_bytes, void *stream);
 
-/* 0 for sizes that blockint8_moe_layer_fp8_routed rejects, and for T = 0. */
+/* 0 for sizes that blockint8_moe_layer_fp8_routed rejects, and for T = 0.  It falls where
+ * the products take another kernel: a workspace for several sizes is of the largest. */
 int64_t blockint8_moe_layer_fp8_routed_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
 
 #ifdef __cplusplus
