@@ -252,10 +252,7 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int64_t t, int t
         if (!sigmoid && !p.renormalize) {
             double part = 0.0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float e = expf(fminf(l[v], FLT_MAX) - m);
-                part += (double)pick(l[v] > -INFINITY, e, 0.0f);
-            }
+            for (int v = 0; v < V; ++v) part += softmax_score(l[v], m);
             total = sum<G>(part);
             total = pick(total > 0.0, total, 1.0);
         }
