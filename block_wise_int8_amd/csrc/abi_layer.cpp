@@ -108,7 +108,7 @@ int32_t blockint8_qk_norm_rope(const uint16_t *q, int64_t q_token, int64_t q_hea
 }
 
 int64_t blockint8_moe_route_grouped_workspace_size(int64_t T, int32_t E) {
-    if (T <= 0 || T > kMaxRows || E < 1 || E > 1024) return 0;
+    if (T <= 0 || T > BI8_MAX_ROUTE_TOKENS || E < 1 || E > 1024) return 0;
     return bi8::route_grouped_workspace_bytes(T, E);
 }
 
@@ -120,7 +120,8 @@ int32_t blockint8_moe_route_grouped(const void *logits, int32_t logits_bf16, int
     static const char fn[] = "blockint8_moe_route_grouped";
     if (E < 1 || E > 1024) return fail_status(BI8_ERR_SHAPE, "%s: E = %d out of range [1, 1024]", fn, E);
     if (k < 1 || k > 32 || k > E) return fail_status(BI8_ERR_SHAPE, "%s: k = %d out of range [1, min(E, 32)]", fn, k);
-    if (T < 0 || T > kMaxRows / k) return fail_status(BI8_ERR_SHAPE, "%s: T = %lld out of range", fn, (long long)T);
+    if (T < 0 || T > kMaxRows / k || T > BI8_MAX_ROUTE_TOKENS)
+        return fail_status(BI8_ERR_SHAPE, "%s: T = %lld out of range", fn, (long long)T);
     if (score != BI8_SCORE_SOFTMAX && score != BI8_SCORE_SIGMOID)
         return fail_status(BI8_ERR_SHAPE, "%s: unknown score %d", fn, score);
     if (groups < 1 || groups > 64 || E % groups != 0)

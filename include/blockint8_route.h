@@ -15,6 +15,9 @@ extern "C" {
 
 enum { BI8_SCORE_SOFTMAX = 0, BI8_SCORE_SIGMOID = 1 };
 
+/* Most tokens of a call: its launches are of fewer than 2^32 threads. */
+#define BI8_MAX_ROUTE_TOKENS ((1 << 28) - 64)
+
 /*
  * Router and dispatch order: one launch for a few tokens, else two (three from
  * 2^14 tokens on).  For each token t with logits l:
@@ -50,9 +53,9 @@ enum { BI8_SCORE_SOFTMAX = 0, BI8_SCORE_SIGMOID = 1 };
  *                 contents undefined before and after.  Calls that share one
  *                 must not overlap in time.  NULL where that size is 0.
  *
- * Limits: 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k < 2^31, groups a divisor
- * of E of at most 64, 1 <= topk_groups <= groups, k experts at least in the kept
- * groups.  T == 0 writes expert_offsets (all zero).
+ * Limits: 1 <= E <= 1024, 1 <= k <= min(E, 32), T <= BI8_MAX_ROUTE_TOKENS, T * k <
+ * 2^31, groups a divisor of E of at most 64, 1 <= topk_groups <= groups, k experts
+ * at least in the kept groups.  T == 0 writes expert_offsets (all zero).
  *
  * Errors: NULL pointer -> BI8_ERR_NULL; a limit broken, ldl < E, an unknown
  * score, group_top not 1 or 2, a scale that is not finite, a workspace too small
