@@ -37,8 +37,8 @@ extern "C" {
  *   q_weight   bf16 [D] or NULL (no norm); k_weight the same for the key heads
  *   table      fp32 [P, rot]: cosines, then sines, of the rot / 2 pairs
  *   positions  int32, axis a of token t at positions[a * positions_axis + t].
- *              A token with a position outside [0, P) is left out: nothing is
- *              read from the table and its outputs are not written (padding).
+ *              A token with a position outside [0, P) is left out: its outputs
+ *              are not written (padding), and row 0 of the table is read for it.
  *   sections   int32 [axes] in HOST memory: axis 0 turns the first sections[0]
  *              pairs, axis 1 the next sections[1], ...; their sum is rot / 2.
  *              Text has one axis, {rot / 2}; images and video have three (time,
