@@ -19,10 +19,12 @@
 // two bf16 values that hold 16 bits of it, which take the two halves of a longer
 // sum over the ranks, each against the same b.
 //
-// Bound by HBM: x read once, y read and written once, the adapters in use once.  4096
-// rows, K = 4096, 28672 columns, rank 64 in 6 runs: 28 to 35 us and about 115 (y alone,
-// read and written in the same order, 88); 64 rows of 64 adapters, 6144 columns, rank
-// 16: 8.5 and 7.2 (40 MB of adapters); 1 row 4.5 and 4.8, the latency of two launches.
+// Long batches are bound by HBM: x read once, y read and written once, the adapters in
+// use once.  4096 rows, K = 4096, 28672 columns, rank 64 in 6 runs: 28 to 35 us and
+// about 115 (y alone, read and written in the same order, 88).  Short ones are bound by
+// their chains of loads: 64 rows of 64 adapters, 6144 columns, rank 16: 8 to 10 and 7
+// (25 MB of a, 2.6 to 3.2 TB/s; 12.6 of b and 1.6 of y, 2.0); 1 row 4.6 and 4.8, the
+// latency of two launches.
 #include <algorithm>
 
 #include "codes.hpp"
@@ -133,7 +135,7 @@ __device__ __forceinline__ u32x4 load_at(__amdgpu_buffer_rsrc_t r, uint32_t offs
 // them behind its issue; the compiler keeps writes of them two wait states away, but not
 // behind a store with a scalar offset, where it takes them to be free at once.  They are
 // not: the next instruction's 2^31 (the offset of a load that is not there) was stored in
-// the place of the first register, two values of y as zeros, in a quarter of all calls of
+// the place of the first register, two values of y as zeros, in a fifth of all calls of
 // 333 rows and 5000 columns.
 __device__ __forceinline__ void store_at(__amdgpu_buffer_rsrc_t r, uint32_t offset, const u32x4 &v) {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)offset, 0, 0);

@@ -19,8 +19,8 @@ enum { BI8_SCORE_SOFTMAX = 0, BI8_SCORE_SIGMOID = 1 };
 #define BI8_MAX_ROUTE_TOKENS ((1 << 28) - 64)
 
 /*
- * Router and dispatch order: one launch for a few tokens, else two (three from
- * 2^14 tokens on).  For each token t with logits l:
+ * Router and dispatch order: one launch for a few tokens, else two (three for
+ * more than 2^14).  For each token t with logits l:
  *
  *   score   p[e] = exp(l[e] - max l) / sum exp(l - max l)   (softmax)
  *           p[e] = 1 / (1 + exp(-l[e]))                     (sigmoid)
