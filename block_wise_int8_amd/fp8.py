@@ -230,7 +230,9 @@ def moe_gemm_silu_quant_fp8(xq: torch.Tensor, xs: torch.Tensor, expert_offsets: 
 
 
 def moe_layer_fp8_workspace_size(T: int, H: int, I: int, E: int, k: int, routed: bool = False) -> int:
-    """Bytes of workspace ``moe_layer_fp8`` needs for T tokens (``routed``: with a given ``route``)."""
+    """Bytes of workspace ``moe_layer_fp8`` needs for T tokens (``routed``: with a given ``route``).
+
+    It falls where the products take another kernel: a workspace for several sizes is of the largest."""
     lib = _bi8.load()
     fn = lib.blockint8_moe_layer_fp8_routed_workspace_size if routed else lib.blockint8_moe_layer_fp8_workspace_size
     return int(fn(T, H, I, E, k))

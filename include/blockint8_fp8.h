@@ -200,7 +200,8 @@ int32_t blockint8_moe_layer_fp8(const uint16_t *x, int64_t ldx, const float *log
                                 int64_t H, int64_t I, int32_t E, int32_t k, int32_t renormalize, int32_t block_n,
                                 int32_t block_k, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* 0 for sizes that blockint8_moe_layer_fp8 rejects, and for T = 0. */
+/* 0 for sizes that blockint8_moe_layer_fp8 rejects, and for T = 0.  It falls where the
+ * products take another kernel: a workspace for several sizes is of the largest. */
 int64_t blockint8_moe_layer_fp8_workspace_size(int64_t T, int64_t H, int64_t I, int32_t E, int32_t k);
 
 /*
